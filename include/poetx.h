@@ -512,6 +512,126 @@ int poetx_adam_step(float* theta, const float* grad, float* m, float* v, int64_t
                     int64_t step, float lr, float beta1, float beta2, float eps,
                     void* stream);
 
+/*
+ * Optimizer steps over many tensors at once.  A set of tensors is described
+ * once (poetx_param_table) and stepped with one launch per call, whatever the
+ * number of tensors: the generators of every layer, adapters, any others.
+ *
+ * The moments of a set live in the caller's flat state arrays: each tensor
+ * takes ceil(count / 256) blocks of 256 values, the tensors one after another
+ * in the set's order; the values after a tensor's last are padding.
+ *   POETX_STATE_F32  m, v: fp32 [blocks][256]
+ *   POETX_STATE_8BIT m, v: one byte per value, [blocks][256]; m_exp, v_exp:
+ *                    one byte E per block, the exponent (fp32 bias) of its
+ *                    largest code.  A code holds an exponent field e and a
+ *                    3-bit fraction f; its value is
+ *                      m: bit 7 the sign, e in bits 6..3:
+ *                         (8 + f) 2^(E-127-18+e) for e > 0, f 2^(E-127-17) for e = 0
+ *                      v: e in bits 7..3, no sign:
+ *                         (8 + f) 2^(E-127-34+e) for e > 0, f 2^(E-127-33) for e = 0
+ *                    E = 255 marks a block that holds NaN; E below 40 is
+ *                    read as 40 (a state of zero bytes is a state of zeros).
+ * 8-bit codes are rounded by a dither u in [0, 1) that runs through the
+ * multiples of two irrationals with the value's position in the state array
+ * and with the step: round up where the dropped fraction plus u reaches 1.
+ * Over the steps a value is so kept on average; rounding to nearest, a second
+ * moment with beta2 = 0.999 could not leave its code (a step moves it by 0.1 %,
+ * half a code is 6 %).  A nonzero second moment never rounds to zero.  The
+ * same dither rounds bf16 tensors.  Nothing is random: equal inputs give equal
+ * bits.
+ */
+typedef struct {
+  void* param;        /* [count], device, updated in place (NULL: a set for
+                         poetx_grad_norm alone)                                  */
+  const void* grad;   /* [count], device                                         */
+  void* copy_bf16;    /* fp32 tensors: bf16 copy [count] written with the update
+                         (rounded to nearest even), device, nullable             */
+  int64_t count;      /* >= 0                                                    */
+  float lr_mul;       /* the tensor's multiple of the step's learning rate       */
+  float weight_decay; /* decoupled decay: p loses lr lr_mul weight_decay p       */
+  int32_t param_dtype; /* poetx_dtype of param                                   */
+  int32_t grad_dtype;  /* poetx_dtype of grad                                    */
+} poetx_param;
+
+/* A set of tensors, filled by poetx_param_table; `table` is the caller's. */
+typedef struct {
+  const void* table; /* DEVICE copy of the host table, 256-byte aligned           */
+  int64_t blocks;    /* blocks of 256 values in each state array                  */
+  int64_t chunks;
+  int64_t values;    /* sum of count                                             */
+  int32_t count;     /* tensors                                                  */
+  uint32_t norm_only; /* some tensor has no param: poetx_grad_norm takes the set alone */
+} poetx_param_set;
+
+#define POETX_STATE_F32 0
+#define POETX_STATE_8BIT 1
+
+/* Moments of a set, device. */
+typedef struct {
+  void* m;
+  void* v;
+  void* m_exp; /* POETX_STATE_8BIT only */
+  void* v_exp; /* POETX_STATE_8BIT only */
+  int32_t kind; /* POETX_STATE_F32 or POETX_STATE_8BIT */
+  uint32_t reserved; /* must be 0 */
+} poetx_adamw_state;
+
+typedef struct {
+  float lr, beta1, beta2, eps;
+} poetx_adamw_hyper;
+
+/*
+ * poetx_param_table_bytes: bytes of the table of these tensors (0 and the last
+ *   error set if one is invalid).  Host only.
+ * poetx_param_table: writes the table (host memory, `bytes` of it) and *set
+ *   (with table NULL).  The caller copies the bytes to the device once, and
+ *   puts that address into set->table; the table is then reused by every call
+ *   until a tensor moves.  Host only; nothing is enqueued.
+ *   params  host array of count poetx_param (count in [0, 1048576]); at most
+ *           2^37 values in all.  Pointers need the alignment of their type;
+ *           tensors whose pointers are all 16-byte aligned go faster.
+ * Tensors must not overlap each other, nor the gradients or state.
+ */
+size_t poetx_param_table_bytes(const poetx_param* params, int32_t count);
+int poetx_param_table(const poetx_param* params, int32_t count, void* host_table, size_t bytes,
+                      poetx_param_set* set);
+
+/*
+ * The 2-norm of all gradients of the set together and the coefficient that
+ * clips it, both left on the device:
+ *   out[0] = sqrt(sum g^2),  out[1] = min(1, max_norm / (out[0] + 1e-6))
+ * summed in fp64 in a fixed order.  If the norm is not finite, out[1] is NaN
+ * (poetx_adamw_step then leaves everything as it was).
+ *   max_norm  > 0 (infinity: no clipping)
+ *   out       fp32 [2], device
+ *   ws        poetx_grad_norm_workspace_bytes(set) bytes
+ * The set's table holds the launch's arrival counter: calls on one table must
+ * not run at the same time (on two streams).
+ */
+size_t poetx_grad_norm_workspace_bytes(const poetx_param_set* set);
+int poetx_grad_norm(const poetx_param_set* set, float max_norm, float* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One AdamW step (decoupled weight decay, bias correction) on every tensor of
+ * the set, in place, with g = coef * grad:
+ *   m <- b1 m + (1-b1) g;  v <- b2 v + (1-b2) g^2;
+ *   p <- p - lr lr_mul (weight_decay p + (m / (1-b1^step)) / (sqrt(v / (1-b2^step)) + eps))
+ * in fp32; the update uses the moments before they are rounded to 8 bits.
+ *   step  >= 1, the number of this step
+ *   coef  fp32 [1], device (e.g. out + 1 of poetx_grad_norm), nullable (1).
+ *         If it is not finite, nothing is written.
+ */
+int poetx_adamw_step(const poetx_param_set* set, const poetx_adamw_state* state, const poetx_adamw_hyper* hyper,
+                     int64_t step, const float* coef, void* stream);
+
+/*
+ * The moments an 8-bit state stands for, as bf16 [blocks][256] (exact: a code
+ * has four significant bits; blocks with E = 255 give NaN).
+ *   m_out, v_out  device, 16-byte aligned, each nullable
+ */
+int poetx_adamw_moments(const poetx_param_set* set, const poetx_adamw_state* state, void* m_out, void* v_out,
+                        void* stream);
+
 /* Message of the last error on this thread ("" if none). */
 const char* poetx_last_error(void);
 

@@ -19,6 +19,8 @@ POETX_W0_INT8 = 2
 POETX_SEPARATE_BLOCK_PRODUCTS = 4
 POETX_W0_TRANSPOSED = 8
 POETX_X_PERMUTED = 16
+POETX_STATE_F32 = 0
+POETX_STATE_8BIT = 1
 OP_FORWARD, OP_BACKWARD, OP_MERGE, OP_FORWARD_BLOCKS, OP_BACKWARD_BLOCKS, OP_MERGE_BLOCKS, OP_BACKWARD_DQ = range(7)
 
 _STATUS = {0: "POETX_OK", -1: "POETX_EINVAL", -2: "POETX_ESHAPE", -3: "POETX_EDTYPE",
@@ -33,6 +35,8 @@ EXPORTED = ("poetx_workspace_bytes", "poetx_build_workspace_bytes", "poetx_build
             "poetx_chain_workspace_bytes", "poetx_merge", "poetx_merge_blocks", "poetx_merge_blocks_sets",
             "poetx_merge_sets_workspace_bytes", "poetx_make_permutation",
             "poetx_adam_step", "poetx_w0_bytes", "poetx_quantize_w0", "poetx_dequantize_w0", "poetx_transpose_w0",
+            "poetx_param_table_bytes", "poetx_param_table", "poetx_grad_norm_workspace_bytes", "poetx_grad_norm",
+            "poetx_adamw_step", "poetx_adamw_moments",
             "poetx_last_error", "poetx_timing_enable", "poetx_timing_summary")
 
 
@@ -67,6 +71,31 @@ class Blocks(ctypes.Structure):
     """poetx_blocks: prebuilt Cayley blocks of one layer."""
     _fields_ = [("Q32R", ctypes.c_void_p), ("Q32P", ctypes.c_void_p), ("QR", ctypes.c_void_p),
                 ("QP", ctypes.c_void_p), ("QTR", ctypes.c_void_p), ("QTP", ctypes.c_void_p)]
+
+
+class Param(ctypes.Structure):
+    """poetx_param: one tensor of an optimizer set."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("copy_bf16", ctypes.c_void_p),
+                ("count", ctypes.c_int64), ("lr_mul", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class ParamSet(ctypes.Structure):
+    """poetx_param_set: filled by poetx_param_table."""
+    _fields_ = [("table", ctypes.c_void_p), ("blocks", ctypes.c_int64), ("chunks", ctypes.c_int64),
+                ("values", ctypes.c_int64), ("count", ctypes.c_int32), ("norm_only", ctypes.c_uint32)]
+
+
+class AdamwState(ctypes.Structure):
+    """poetx_adamw_state: the moments of a set."""
+    _fields_ = [("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("kind", ctypes.c_int32), ("reserved", ctypes.c_uint32)]
+
+
+class AdamwHyper(ctypes.Structure):
+    """poetx_adamw_hyper."""
+    _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_float), ("beta2", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 def _addr(t):
@@ -136,6 +165,13 @@ def lib():
         "poetx_make_permutation": (ctypes.c_int, [u64, u64, i32, i64, vp]),
         "poetx_adam_step": (ctypes.c_int, [vp, vp, vp, vp, i64, i64, ctypes.c_float, ctypes.c_float,
                                            ctypes.c_float, ctypes.c_float, vp]),
+        "poetx_param_table_bytes": (sz, [ctypes.POINTER(Param), i32]),
+        "poetx_param_table": (ctypes.c_int, [ctypes.POINTER(Param), i32, vp, sz, ctypes.POINTER(ParamSet)]),
+        "poetx_grad_norm_workspace_bytes": (sz, [ctypes.POINTER(ParamSet)]),
+        "poetx_grad_norm": (ctypes.c_int, [ctypes.POINTER(ParamSet), ctypes.c_float, vp, vp, sz, vp]),
+        "poetx_adamw_step": (ctypes.c_int, [ctypes.POINTER(ParamSet), ctypes.POINTER(AdamwState),
+                                            ctypes.POINTER(AdamwHyper), i64, vp, vp]),
+        "poetx_adamw_moments": (ctypes.c_int, [ctypes.POINTER(ParamSet), ctypes.POINTER(AdamwState), vp, vp, vp]),
         "poetx_w0_bytes": (sz, [LP]),
         "poetx_quantize_w0": (ctypes.c_int, [LP, vp, vp, vp]),
         "poetx_dequantize_w0": (ctypes.c_int, [LP, vp, vp, vp]),
@@ -372,6 +408,39 @@ def poetx_adam_step(theta, grad, m, v, count, step, lr=1e-3, beta1=0.9, beta2=0.
     _check("poetx_adam_step", lib().poetx_adam_step(_ptr(theta), _ptr(grad), _ptr(m), _ptr(v), int(count), int(step),
                                                     float(lr), float(beta1), float(beta2), float(eps),
                                                     _stream(stream)))
+
+
+def param_table(params):
+    """(host table as a uint8 tensor, ParamSet without its table) of a sequence of Param."""
+    import torch
+    arr = (Param * max(len(params), 1))(*params)
+    need = lib().poetx_param_table_bytes(arr, len(params))
+    if need == 0:
+        raise PoetxError("poetx_param_table_bytes", -1, last_error())
+    host = torch.empty(need, dtype=torch.uint8)
+    out = ParamSet()
+    _check("poetx_param_table", lib().poetx_param_table(arr, len(params), ctypes.c_void_p(host.data_ptr()), need,
+                                                        ctypes.byref(out)))
+    return host, out
+
+
+def grad_norm_workspace_bytes(pset):
+    return lib().poetx_grad_norm_workspace_bytes(ctypes.byref(pset))
+
+
+def poetx_grad_norm(pset, max_norm, out, ws, stream=None):
+    _check("poetx_grad_norm", lib().poetx_grad_norm(ctypes.byref(pset), float(max_norm), _ptr(out), _ptr(ws),
+                                                    ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def poetx_adamw_step(pset, state, hyper, step, coef=None, stream=None):
+    _check("poetx_adamw_step", lib().poetx_adamw_step(ctypes.byref(pset), ctypes.byref(state), ctypes.byref(hyper),
+                                                      int(step), _ptr(coef), _stream(stream)))
+
+
+def poetx_adamw_moments(pset, state, m_out, v_out, stream=None):
+    _check("poetx_adamw_moments", lib().poetx_adamw_moments(ctypes.byref(pset), ctypes.byref(state), _ptr(m_out),
+                                                            _ptr(v_out), _stream(stream)))
 
 
 def timing_enable(on):

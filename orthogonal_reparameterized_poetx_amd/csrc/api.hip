@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "../../include/poetx.h"
+#include "host.h"
 #include "kernels.h"
 
 using namespace poetx;
@@ -1649,3 +1650,27 @@ int poetx_timing_summary(char* buf, size_t len) {
 }
 
 }  // extern "C"
+
+// ---- services for the entry points of other files (host.h)
+namespace poetx {
+
+int host_fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_err = buf;
+  return code;
+}
+
+int host_check_launch(const char* what) { return check_launch(what); }
+
+int host_check_ws(void* ws, size_t have, size_t need) { return check_ws(ws, have, need); }
+
+HostTimer::HostTimer(hipStream_t s, const char* name, double flops, double bytes)
+    : t_(g_timing ? new Tm(s, name, flops, bytes) : nullptr) {}
+
+HostTimer::~HostTimer() { delete static_cast<Tm*>(t_); }
+
+}  // namespace poetx

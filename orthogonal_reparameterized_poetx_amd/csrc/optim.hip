@@ -1,0 +1,538 @@
+// Optimizer steps over many tensors with one launch: the global gradient norm
+// with its clipping coefficient, and AdamW (Loshchilov & Hutter 2019) with
+// 32-bit or 8-bit moments.  See include/poetx.h for formats and formulas.
+//
+// Both are streaming passes: per value the step reads p, g, m, v and writes
+// p, m, v, 28 bytes with fp32 everywhere and 16 with 8-bit moments, against
+// about 60 vector instructions, so HBM bounds them.  A table made once on the
+// host maps workgroups to tensors: chunk c of the grid is CHUNK_BLOCKS state
+// blocks of one tensor.
+#include <cmath>
+#include <cstring>
+
+#include "../../include/poetx.h"
+#include "common.h"
+#include "host.h"
+
+namespace poetx {
+
+constexpr int OPT_BLOCK = 256;     // values that share an exponent byte: one wave, four values a lane
+constexpr int OPT_WAVES = 4;
+constexpr int OPT_UNROLL = 4;      // blocks a wave has in flight
+constexpr int CHUNK_BLOCKS = OPT_WAVES * OPT_UNROLL;
+
+struct OptTensor {
+  void* p;
+  const void* g;
+  uint16_t* copy;
+  int64_t count;
+  int64_t block0;    // first state block
+  float lr_mul, decay;
+  int32_t pbf, gbf;  // bf16 parameter / gradient
+  int32_t vec;       // every pointer 16-byte aligned
+  int32_t pad;
+};
+struct OptChunk {
+  int32_t tensor;
+  int32_t block;     // first block of the chunk within the tensor
+};
+struct OptHead {     // start of the table; the tensors and the chunks follow
+  uint32_t arrived;  // workgroups of a running norm that have stored their sum
+  uint32_t pad[63];
+};
+static size_t opt_tensor_offset() { return sizeof(OptHead); }
+static size_t opt_chunk_offset(int64_t count) { return sizeof(OptHead) + (size_t)count * sizeof(OptTensor); }
+
+// ---- the dither: fractional parts of pos alpha + step beta, alpha and beta
+// the powers of the reciprocal plastic number (Roberts 2018), times 2^32.
+// Over steps at one position, and over positions at one step, it fills [0, 1)
+// evenly.  m takes bits 31..12, v bits 24..5 (the same sequence times 2^7, an
+// irrational of its own), a bf16 parameter bits 31..16.
+constexpr uint32_t kAlphaPos = 0xC13FA9A9u, kAlphaStep = 0x91E10DA5u;
+
+template <bool SIGNED>
+struct Code {
+  static constexpr int LOW = SIGNED ? 15 : 31;        // exponent fields
+  static constexpr int FIX = SIGNED ? 271 : 287;      // 127 + 127 + distance of the lowest step from E
+};
+
+// E of a block: the exponent of its largest magnitude after rounding up by
+// the largest dither, so that no code overflows
+__device__ __forceinline__ int block_exp(uint32_t maxbits) {
+  if (maxbits >= 0x7f800000u) return 255;
+  const int e = (int)((maxbits + 0xFFFFFu) >> 23);
+  return e < 40 ? 40 : e > 254 ? 254 : e;
+}
+
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t encode8(float x, uint32_t u, int E) {
+  const uint32_t bits = __float_as_uint(x) & 0x7fffffffu;
+  // normal: add the dither below the third fraction bit and cut it off
+  const int normal = (int)((bits + u) >> 20) - ((E - Code<SIGNED>::LOW) << 3);
+  // below the lowest octave: steps of a fixed size
+  const float unit = __uint_as_float((uint32_t)(Code<SIGNED>::FIX - E) << 23);
+  const int tiny = (int)floorf(__fadd_rn(__fmul_rn(__uint_as_float(bits), unit), (float)u * 0x1p-20f));
+  int c = (int)(bits >> 23) - E + Code<SIGNED>::LOW >= 1 ? normal : tiny;
+  if (SIGNED) {
+    c = c > 127 ? 127 : c;
+    return (uint32_t)c | (x < 0.f ? 128u : 0u);
+  }
+  c = c > 255 ? 255 : c < 1 ? 1 : c;
+  return bits ? (uint32_t)c : 0u;
+}
+
+template <bool SIGNED>
+__device__ __forceinline__ float decode8(uint32_t c, int E) {
+  const uint32_t e = (c >> 3) & Code<SIGNED>::LOW, f = c & 7u;
+  const float tiny = (float)f * __uint_as_float((uint32_t)(E - Code<SIGNED>::LOW - 2) << 23);
+  const float normal = __uint_as_float(((uint32_t)(E - Code<SIGNED>::LOW) + e) << 23 | f << 20);
+  float v = e ? normal : tiny;
+  if (SIGNED) v = __uint_as_float(__float_as_uint(v) | (c & 128u) << 24);
+  return v;
+}
+// a stored exponent byte as it is read: at least 40; 255 makes the block NaN
+__device__ __forceinline__ int exp_of(int byte) { return byte < 40 ? 40 : byte; }
+
+// largest of x over the wave, in every lane
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+#define POETX_DPP_MAX(ctrl, rows) \
+  { const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, rows, 0xf, false); x = x > y ? x : y; }
+  POETX_DPP_MAX(0x111, 0xf)   // row_shr 1, 2, 4, 8: lane 15 of each row of 16 holds the row's
+  POETX_DPP_MAX(0x112, 0xf)
+  POETX_DPP_MAX(0x114, 0xf)
+  POETX_DPP_MAX(0x118, 0xf)
+  POETX_DPP_MAX(0x142, 0xa)   // row 0 into 1, 2 into 3
+  POETX_DPP_MAX(0x143, 0xc)   // rows 0, 1 into 2, 3
+#undef POETX_DPP_MAX
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+struct F4 { float x[4]; };
+
+// four values from `at` on; those at or past `left` read as zero
+__device__ __forceinline__ F4 load4(const void* base, int64_t at, int left, bool bf, bool vec) {
+  F4 r;
+  if (vec && left >= 4) {
+    if (bf) {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+      r.x[0] = __uint_as_float(w.x << 16); r.x[1] = __uint_as_float(w.x & 0xffff0000u);
+      r.x[2] = __uint_as_float(w.y << 16); r.x[3] = __uint_as_float(w.y & 0xffff0000u);
+    } else {
+      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+      r.x[0] = w.x; r.x[1] = w.y; r.x[2] = w.z; r.x[3] = w.w;
+    }
+    return r;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    r.x[j] = j >= left ? 0.f : bf ? bits_to_f32(static_cast<const uint16_t*>(base)[at + j])
+                                  : static_cast<const float*>(base)[at + j];
+  return r;
+}
+
+__device__ __forceinline__ void store4_bf16(uint16_t* base, int64_t at, int left, bool vec, const uint16_t h[4]) {
+  if (vec && left >= 4) {
+    *reinterpret_cast<uint2*>(base + at) = make_uint2(pack2(h[0], h[1]), pack2(h[2], h[3]));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < left) base[at + j] = h[j];
+}
+
+struct StepArgs {
+  const OptTensor* tensors;
+  const OptChunk* chunks;
+  const float* coef;
+  void *m, *v;
+  uint8_t *me, *ve;
+  float lr, b1, b2, ob1, ob2, eps, ibc1, ibc2;
+  uint32_t step;
+};
+
+// The moments are formed with separate roundings (no contraction): the codes
+// of the 8-bit state then follow from the formula alone.
+template <bool Q8>
+__global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
+#pragma clang fp contract(off)
+  const float coef = a.coef ? *a.coef : 1.f;
+  if (!(fabsf(coef) < INFINITY)) return;
+  const OptChunk ch = a.chunks[blockIdx.x];
+  const OptTensor t = a.tensors[ch.tensor];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float lr = a.lr * t.lr_mul;
+  F4 p[OPT_UNROLL], g[OPT_UNROLL], m[OPT_UNROLL], v[OPT_UNROLL];
+  uint32_t mc[OPT_UNROLL], vc[OPT_UNROLL];
+  int Em[OPT_UNROLL], Ev[OPT_UNROLL];
+  int left[OPT_UNROLL];   // values of the tensor from this lane's first on
+#pragma unroll
+  for (int i = 0; i < OPT_UNROLL; ++i) {
+    const int64_t blk = ch.block + wave * OPT_UNROLL + i;
+    const int64_t at = blk * OPT_BLOCK + lane * 4;
+    const int64_t l = t.count - at;
+    left[i] = l < 0 ? 0 : l > 4 ? 4 : (int)l;
+    if (blk * OPT_BLOCK >= t.count) continue;
+    p[i] = load4(t.p, at, left[i], t.pbf, t.vec);
+    g[i] = load4(t.g, at, left[i], t.gbf, t.vec);
+    const int64_t s = (t.block0 + blk) * OPT_BLOCK + lane * 4;
+    if (Q8) {
+      Em[i] = a.me[t.block0 + blk];
+      Ev[i] = a.ve[t.block0 + blk];
+      mc[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s);
+      vc[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s);
+    } else {
+      const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.m) + s);
+      const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + s);
+      m[i].x[0] = x.x; m[i].x[1] = x.y; m[i].x[2] = x.z; m[i].x[3] = x.w;
+      v[i].x[0] = y.x; v[i].x[1] = y.y; v[i].x[2] = y.z; v[i].x[3] = y.w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < OPT_UNROLL; ++i) {
+    const int64_t blk = ch.block + wave * OPT_UNROLL + i;
+    if (blk * OPT_BLOCK >= t.count) break;
+    const int64_t at = blk * OPT_BLOCK + lane * 4;
+    const int64_t sb = t.block0 + blk, s = sb * OPT_BLOCK + lane * 4;
+    if (Q8) {
+      const int em = exp_of(Em[i]), ev = exp_of(Ev[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        m[i].x[j] = em == 255 ? NAN : decode8<true>(mc[i] >> (8 * j) & 255u, em);
+        v[i].x[j] = ev == 255 ? NAN : decode8<false>(vc[i] >> (8 * j) & 255u, ev);
+      }
+    }
+    const uint32_t h0 = (uint32_t)s * kAlphaPos + a.step * kAlphaStep;
+    uint16_t pb[4], cb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float gj = g[i].x[j] * coef;
+      float mj = m[i].x[j] * a.b1 + gj * a.ob1;
+      float vj = v[i].x[j] * a.b2 + gj * gj * a.ob2;
+      if (j >= left[i]) mj = vj = 0.f;   // padding
+      m[i].x[j] = mj;
+      v[i].x[j] = vj;
+      const float up = (mj * a.ibc1) / (sqrtf(vj * a.ibc2) + a.eps);
+      const float q = p[i].x[j] - lr * (t.decay * p[i].x[j] + up);
+      p[i].x[j] = q;
+      // the carry of the dither must not turn infinity or NaN into another value
+      const uint32_t qb = __float_as_uint(q);
+      const uint32_t d = (h0 + (uint32_t)j * kAlphaPos) >> 16;
+      pb[j] = (uint16_t)((qb & 0x7f800000u) == 0x7f800000u ? f32_to_bits(q) : (qb + d) >> 16);
+      cb[j] = f32_to_bits(q);
+    }
+    if (t.pbf) {
+      store4_bf16(static_cast<uint16_t*>(t.p), at, left[i], t.vec, pb);
+    } else {
+      float* dst = static_cast<float*>(t.p) + at;
+      if (t.vec && left[i] == 4) {
+        *reinterpret_cast<float4*>(dst) = make_float4(p[i].x[0], p[i].x[1], p[i].x[2], p[i].x[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < left[i]) dst[j] = p[i].x[j];
+      }
+      if (t.copy) store4_bf16(t.copy, at, left[i], t.vec, cb);
+    }
+    if (Q8) {
+      uint32_t xm = 0, xv = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t bm = __float_as_uint(m[i].x[j]) & 0x7fffffffu, bv = __float_as_uint(v[i].x[j]) & 0x7fffffffu;
+        xm = xm > bm ? xm : bm;
+        xv = xv > bv ? xv : bv;
+      }
+      const int em = block_exp(wave_max(xm)), ev = block_exp(wave_max(xv));
+      uint32_t om = 0, ov = 0;
+      if (em != 255) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          om |= encode8<true>(m[i].x[j], (h0 + (uint32_t)j * kAlphaPos) >> 12, em) << (8 * j);
+      }
+      if (ev != 255) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          ov |= encode8<false>(v[i].x[j], (h0 + (uint32_t)j * kAlphaPos) >> 5 & 0xFFFFFu, ev) << (8 * j);
+      }
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s) = om;
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s) = ov;
+      if (lane == 0) {
+        a.me[sb] = (uint8_t)em;
+        a.ve[sb] = (uint8_t)ev;
+      }
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.m) + s) =
+          make_float4(m[i].x[0], m[i].x[1], m[i].x[2], m[i].x[3]);
+      *reinterpret_cast<float4*>(static_cast<float*>(a.v) + s) =
+          make_float4(v[i].x[0], v[i].x[1], v[i].x[2], v[i].x[3]);
+    }
+  }
+}
+
+// Squares are exact in fp64 and cannot overflow; their sums keep far more
+// bits than the fp32 result, whatever the count.  Workgroup w sums the chunks
+// w, w + grid, ...; the last to arrive adds the partial sums in index order,
+// so the result does not depend on the order of arrival.
+__global__ __launch_bounds__(256) void grad_norm_kernel(OptHead* head, const OptTensor* tensors, const OptChunk* chunks,
+                                                        int64_t nchunks, float max_norm, double* part, float* out) {
+  __shared__ double red[OPT_WAVES];
+  __shared__ uint32_t last;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double sum = 0.0;
+  for (int64_t c = blockIdx.x; c < nchunks; c += gridDim.x) {
+    const OptChunk ch = chunks[c];
+    const OptTensor t = tensors[ch.tensor];
+    F4 g[OPT_UNROLL];
+#pragma unroll
+    for (int i = 0; i < OPT_UNROLL; ++i) {
+      const int64_t at = ((int64_t)ch.block + wave * OPT_UNROLL + i) * OPT_BLOCK + lane * 4;
+      const int64_t l = t.count - at;
+      g[i] = load4(t.g, at, l < 0 ? 0 : l > 4 ? 4 : (int)l, t.gbf, t.vec);
+    }
+#pragma unroll
+    for (int i = 0; i < OPT_UNROLL; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum = fma((double)g[i].x[j], (double)g[i].x[j], sum);
+  }
+  auto block_sum = [&](double x) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
+    if (lane == 0) red[wave] = x;
+    __syncthreads();
+    x = (red[0] + red[1]) + (red[2] + red[3]);
+    __syncthreads();
+    return x;
+  };
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(&part[blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = __hip_atomic_fetch_add(&head->arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  sum = 0.0;
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += 256)
+    sum += __hip_atomic_load(&part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) {
+    const double norm = sqrt(sum);
+    out[0] = (float)norm;
+    const double c = (double)max_norm / (norm + 1e-6);
+    out[1] = !(norm < INFINITY) ? NAN : c < 1.0 ? (float)c : 1.f;
+    __hip_atomic_store(&head->arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // for the next call
+  }
+}
+
+// what 16 codes from `at` on stand for, in bf16
+template <bool SIGNED>
+__device__ __forceinline__ void moments16(const uint8_t* codes, const uint8_t* exps, uint16_t* out, int64_t at) {
+  const int E = exp_of(exps[at / OPT_BLOCK]);
+  const uint4 c = ldg16(codes + at);
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uint32_t h[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float x = decode8<SIGNED>(w[k / 2] >> (16 * (k & 1) + 8 * e) & 255u, E);
+      h[e] = E == 255 ? 0x7fc0u : __float_as_uint(x) >> 16;   // at most four significant bits: exact
+    }
+    o[k] = h[0] | h[1] << 16;
+  }
+  stg16(out + at, make_uint4(o[0], o[1], o[2], o[3]));
+  stg16(out + at + 8, make_uint4(o[4], o[5], o[6], o[7]));
+}
+
+__global__ __launch_bounds__(256) void moments_kernel(const uint8_t* m, const uint8_t* v, const uint8_t* me,
+                                                      const uint8_t* ve, uint16_t* mo, uint16_t* vo, int64_t blocks) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 16;
+  if (at >= blocks * OPT_BLOCK) return;
+  if (mo) moments16<true>(m, me, mo, at);
+  if (vo) moments16<false>(v, ve, vo, at);
+}
+
+}  // namespace poetx
+
+using namespace poetx;
+
+namespace {
+
+constexpr int kNormGroups = 2048;   // workgroups of a norm: eight per compute unit
+
+int check_param(const poetx_param& p, int32_t i) {
+  if (p.count < 0) return host_fail(POETX_ESHAPE, "tensor %d: count=%lld", (int)i, (long long)p.count);
+  if ((p.param_dtype != POETX_F32 && p.param_dtype != POETX_BF16) ||
+      (p.grad_dtype != POETX_F32 && p.grad_dtype != POETX_BF16))
+    return host_fail(POETX_EDTYPE, "tensor %d: unsupported dtype", (int)i);
+  if (p.copy_bf16 && p.param_dtype != POETX_F32)
+    return host_fail(POETX_EDTYPE, "tensor %d: copy_bf16 goes with an fp32 tensor", (int)i);
+  if (p.count == 0) return POETX_OK;
+  if (!p.grad) return host_fail(POETX_EINVAL, "tensor %d: NULL gradient", (int)i);
+  const uintptr_t pa = p.param_dtype == POETX_F32 ? 3 : 1, ga = p.grad_dtype == POETX_F32 ? 3 : 1;
+  if ((reinterpret_cast<uintptr_t>(p.param) & pa) || (reinterpret_cast<uintptr_t>(p.grad) & ga) ||
+      (reinterpret_cast<uintptr_t>(p.copy_bf16) & 1))
+    return host_fail(POETX_EINVAL, "tensor %d: pointer not aligned to its type", (int)i);
+  return POETX_OK;
+}
+
+// blocks, chunks and values of the tensors
+int plan_params(const poetx_param* params, int32_t count, int64_t* blocks, int64_t* chunks, int64_t* values) {
+  if (count < 0 || count > (1 << 20)) return host_fail(POETX_ESHAPE, "count=%d out of range [0, 1048576]", (int)count);
+  if (count > 0 && !params) return host_fail(POETX_EINVAL, "params is NULL");
+  *blocks = *chunks = *values = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const int rc = check_param(params[i], i);
+    if (rc) return rc;
+    if (params[i].count > (int64_t(1) << 37) - *values)
+      return host_fail(POETX_ESHAPE, "more than 2^37 values in one set");
+    const int64_t b = (params[i].count + OPT_BLOCK - 1) / OPT_BLOCK;
+    *blocks += b;
+    *chunks += (b + CHUNK_BLOCKS - 1) / CHUNK_BLOCKS;
+    *values += params[i].count;
+  }
+  return POETX_OK;
+}
+
+int check_set(const poetx_param_set* set) {
+  if (!set) return host_fail(POETX_EINVAL, "set is NULL");
+  if (set->count < 0 || set->chunks < 0 || set->chunks > 0x7fffffffLL || set->blocks < 0 || set->norm_only > 1)
+    return host_fail(POETX_EINVAL, "set was not made by poetx_param_table");
+  if (set->chunks > 0 && (!set->table || (reinterpret_cast<uintptr_t>(set->table) & (kWsAlign - 1))))
+    return host_fail(POETX_EINVAL, "set->table is NULL or not %zu-byte aligned", kWsAlign);
+  return POETX_OK;
+}
+
+int check_state(const poetx_param_set* set, const poetx_adamw_state* st) {
+  if (!st) return host_fail(POETX_EINVAL, "state is NULL");
+  if (st->reserved) return host_fail(POETX_EINVAL, "state.reserved must be 0");
+  if (st->kind != POETX_STATE_F32 && st->kind != POETX_STATE_8BIT)
+    return host_fail(POETX_EINVAL, "state.kind=%d", (int)st->kind);
+  if (set->blocks == 0) return POETX_OK;
+  if (!st->m || !st->v || (st->kind == POETX_STATE_8BIT && (!st->m_exp || !st->v_exp)))
+    return host_fail(POETX_EINVAL, "NULL state array");
+  if ((reinterpret_cast<uintptr_t>(st->m) & 15) || (reinterpret_cast<uintptr_t>(st->v) & 15))
+    return host_fail(POETX_EINVAL, "state arrays must be 16-byte aligned");
+  return POETX_OK;
+}
+
+const OptTensor* tensors_of(const poetx_param_set* set) {
+  return reinterpret_cast<const OptTensor*>(static_cast<const char*>(set->table) + opt_tensor_offset());
+}
+const OptChunk* chunks_of(const poetx_param_set* set) {
+  return reinterpret_cast<const OptChunk*>(static_cast<const char*>(set->table) + opt_chunk_offset(set->count));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t poetx_param_table_bytes(const poetx_param* params, int32_t count) {
+  int64_t blocks, chunks, values;
+  if (plan_params(params, count, &blocks, &chunks, &values)) return 0;
+  return opt_chunk_offset(count) + (size_t)chunks * sizeof(OptChunk);
+}
+
+int poetx_param_table(const poetx_param* params, int32_t count, void* host_table, size_t bytes,
+                      poetx_param_set* set) {
+  int64_t blocks, chunks, values;
+  const int rc = plan_params(params, count, &blocks, &chunks, &values);
+  if (rc) return rc;
+  if (!host_table || !set) return host_fail(POETX_EINVAL, "NULL argument");
+  const size_t need = opt_chunk_offset(count) + (size_t)chunks * sizeof(OptChunk);
+  if (bytes < need) return host_fail(POETX_EWORKSPACE, "table has %zu bytes, needs %zu", bytes, need);
+  memset(host_table, 0, need);
+  OptTensor* t = reinterpret_cast<OptTensor*>(static_cast<char*>(host_table) + opt_tensor_offset());
+  OptChunk* c = reinterpret_cast<OptChunk*>(static_cast<char*>(host_table) + opt_chunk_offset(count));
+  int64_t b0 = 0;
+  uint32_t norm_only = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const poetx_param& p = params[i];
+    const int64_t nb = (p.count + OPT_BLOCK - 1) / OPT_BLOCK;
+    t[i] = OptTensor{p.param, p.grad, static_cast<uint16_t*>(p.copy_bf16), p.count, b0, p.lr_mul, p.weight_decay,
+                     p.param_dtype == POETX_BF16, p.grad_dtype == POETX_BF16,
+                     !((reinterpret_cast<uintptr_t>(p.param) | reinterpret_cast<uintptr_t>(p.grad) |
+                        reinterpret_cast<uintptr_t>(p.copy_bf16)) & 15), 0};
+    for (int64_t b = 0; b < nb; b += CHUNK_BLOCKS) *c++ = OptChunk{i, (int32_t)b};
+    b0 += nb;
+    if (p.count > 0 && !p.param) norm_only = 1;
+  }
+  *set = poetx_param_set{nullptr, blocks, chunks, values, count, norm_only};
+  return POETX_OK;
+}
+
+size_t poetx_grad_norm_workspace_bytes(const poetx_param_set* set) {
+  return kNormGroups * sizeof(double);
+}
+
+int poetx_grad_norm(const poetx_param_set* set, float max_norm, float* out, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_set(set);
+  if (rc) return rc;
+  if (!(max_norm > 0.f)) return host_fail(POETX_EINVAL, "max_norm must be positive");
+  if (!out) return host_fail(POETX_EINVAL, "out is NULL");
+  if (!set->table) return host_fail(POETX_EINVAL, "set->table is NULL");
+  if ((rc = host_check_ws(ws, ws_bytes, poetx_grad_norm_workspace_bytes(set)))) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t grid = set->chunks < 1 ? 1 : set->chunks < kNormGroups ? set->chunks : kNormGroups;
+  {
+    HostTimer tm(s, "grad_norm", 2.0 * set->values, 0.0);
+    hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)grid), dim3(256), 0, s,
+                       static_cast<OptHead*>(const_cast<void*>(set->table)), tensors_of(set), chunks_of(set),
+                       set->chunks, max_norm, static_cast<double*>(ws), out);
+  }
+  return host_check_launch("gradient norm");
+}
+
+int poetx_adamw_step(const poetx_param_set* set, const poetx_adamw_state* state, const poetx_adamw_hyper* hyper,
+                     int64_t step, const float* coef, void* stream) {
+  int rc = check_set(set);
+  if (rc) return rc;
+  if ((rc = check_state(set, state))) return rc;
+  if (set->norm_only) return host_fail(POETX_EINVAL, "a tensor of the set has no param");
+  if (!hyper) return host_fail(POETX_EINVAL, "hyper is NULL");
+  if (step < 1) return host_fail(POETX_EINVAL, "step must be >= 1");
+  if (!(hyper->beta1 >= 0.f && hyper->beta1 < 1.f && hyper->beta2 >= 0.f && hyper->beta2 < 1.f))
+    return host_fail(POETX_EINVAL, "betas must lie in [0, 1)");
+  if (!(hyper->eps >= 0.f)) return host_fail(POETX_EINVAL, "eps must not be negative");
+  if (set->chunks == 0) return POETX_OK;
+  StepArgs a{};
+  a.tensors = tensors_of(set);
+  a.chunks = chunks_of(set);
+  a.coef = coef;
+  a.m = state->m; a.v = state->v;
+  a.me = static_cast<uint8_t*>(state->m_exp); a.ve = static_cast<uint8_t*>(state->v_exp);
+  a.lr = hyper->lr; a.b1 = hyper->beta1; a.b2 = hyper->beta2; a.eps = hyper->eps;
+  a.ob1 = 1.f - hyper->beta1; a.ob2 = 1.f - hyper->beta2;
+  a.ibc1 = (float)(1.0 / (1.0 - std::pow((double)hyper->beta1, (double)step)));
+  a.ibc2 = (float)(1.0 / (1.0 - std::pow((double)hyper->beta2, (double)step)));
+  a.step = (uint32_t)step;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  {
+    const bool q8 = state->kind == POETX_STATE_8BIT;
+    HostTimer tm(s, "adamw", 0.0, (q8 ? 16.0 : 28.0) * set->values);
+    if (q8) hipLaunchKernelGGL(adamw_kernel<true>, dim3((unsigned)set->chunks), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(adamw_kernel<false>, dim3((unsigned)set->chunks), dim3(256), 0, s, a);
+  }
+  return host_check_launch("adamw");
+}
+
+int poetx_adamw_moments(const poetx_param_set* set, const poetx_adamw_state* state, void* m_out, void* v_out,
+                        void* stream) {
+  int rc = check_set(set);
+  if (rc) return rc;
+  if ((rc = check_state(set, state))) return rc;
+  if (state->kind != POETX_STATE_8BIT) return host_fail(POETX_EINVAL, "poetx_adamw_moments takes an 8-bit state");
+  if ((reinterpret_cast<uintptr_t>(m_out) | reinterpret_cast<uintptr_t>(v_out)) & 15)
+    return host_fail(POETX_EINVAL, "outputs must be 16-byte aligned");
+  if (set->blocks == 0 || (!m_out && !v_out)) return POETX_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  {
+    HostTimer tm(s, "adamw_moments", 0.0, 6.0 * OPT_BLOCK * set->blocks);
+    hipLaunchKernelGGL(moments_kernel, dim3((unsigned)((set->blocks + 15) / 16)), dim3(256), 0, s,
+                       static_cast<const uint8_t*>(state->m), static_cast<const uint8_t*>(state->v),
+                       static_cast<const uint8_t*>(state->m_exp), static_cast<const uint8_t*>(state->v_exp),
+                       static_cast<uint16_t*>(m_out), static_cast<uint16_t*>(v_out), set->blocks);
+  }
+  return host_check_launch("adamw moments");
+}
+
+}  // extern "C"
