@@ -513,6 +513,86 @@ int poetx_adam_step(float* theta, const float* grad, float* m, float* v, int64_t
                     void* stream);
 
 /*
+ * Low-rank adapters of many requests beside one shared projection.  The
+ * batch is cut into segments of consecutive tokens (a request, a sequence);
+ * each segment has one adapter of the set or none:
+ *   forward    y_t += s_a B_a (A_a x_t)
+ *   backward   u_t = s_a B_a^T dy_t,  dx_t += A_a^T u_t,
+ *              dA_a = sum_t u_t x_t^T,  dB_a = sum_t dy_t (s_a A_a x_t)^T
+ * added to what the shared projection (poetx_forward, poetx_backward, any
+ * other) has written to Y and dX.  Adapters of a set may have different ranks.
+ */
+typedef struct {
+  const void* A; /* [r][n] dtype, device, contiguous                              */
+  const void* B; /* [m][r] dtype, device, contiguous                              */
+  float* dA;     /* [r][n] fp32, device, nullable (then not written)              */
+  float* dB;     /* [m][r] fp32, device, nullable (then not written)              */
+  int32_t r;     /* 1..256                                                       */
+  float scale;   /* s                                                            */
+} poetx_adapter;
+
+/* A set of adapters, filled by poetx_adapter_table; `table` and `flags` are the caller's. */
+typedef struct {
+  int64_t m, n;      /* output and input width of the projection                  */
+  int32_t dtype;     /* poetx_dtype of A, B, X, Y, dY, dX                         */
+  int32_t count;     /* adapters                                                 */
+  int32_t max_rank;
+  uint32_t flags;    /* POETX_ACCUMULATE_GRAD: the backward adds into dA and dB   */
+  uint32_t layout;
+  uint32_t reserved;
+  int64_t rows;
+  const void* table; /* DEVICE copy of the host table, 256-byte aligned           */
+} poetx_adapters;
+
+/*
+ * poetx_adapter_table: writes the table of a set (host memory) and *set (table
+ * NULL, flags 0).  The caller copies the bytes to the device and puts that
+ * address into set->table; the table serves every call until a matrix moves
+ * (new values in place need no new table).  Host only.
+ *   count in [0, 65535]; m, n in [1, 32768]
+ * Sets whose matrices are 16-byte aligned, with n (and the ranks) a multiple of
+ * 8 (bf16) or 4 (fp32), go faster.
+ */
+size_t poetx_adapter_table_bytes(int32_t count);
+int poetx_adapter_table(const poetx_adapter* adapters, int32_t count, int64_t m, int64_t n, int32_t dtype,
+                        void* host_table, size_t bytes, poetx_adapters* set);
+
+/*
+ * Workspace bytes of a call of N tokens in nseg segments; op POETX_OP_FORWARD
+ * or POETX_OP_BACKWARD.  0 with the last error set if an argument is invalid.
+ */
+size_t poetx_adapters_workspace_bytes(const poetx_adapters* set, int64_t N, int32_t nseg, int op);
+
+/*
+ * Y[t] += s_a B_a (A_a X[t]) for the adapter a of each token's segment.
+ *   seg_start    [nseg + 1] int32, device: segment i holds the tokens
+ *                seg_start[i] .. seg_start[i+1] - 1 (not decreasing; segments
+ *                may be empty; values are clamped to [0, N])
+ *   seg_adapter  [nseg] int32, device: index into the set; any other value
+ *                (e.g. -1) means no adapter
+ *   X [N][n], rows ldx >= n elements apart;  Y [N][m], rows ldy >= m apart,
+ *   updated in place, not overlapping X.  Tokens of no segment and of
+ *   segments without an adapter are left alone.
+ * A x is summed in fp32 and kept in fp32 (bf16 sets: as the sum of two bf16
+ * values, 16 bits, for the second product); Y is rounded once.  nseg in [0, 1048576].
+ */
+int poetx_adapters_forward(const poetx_adapters* set, const int32_t* seg_start, const int32_t* seg_adapter,
+                           int32_t nseg, const void* X, int64_t ldx, int64_t N, void* Y, int64_t ldy, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of L = <dY, Y> of the forward onto x, A and B.
+ *   dX   [N][n], rows lddx apart: the adapters' share is added in place;
+ *        nullable; must not overlap X or dY
+ *   dA, dB (of the table): overwritten, zero for an adapter without tokens, or
+ *        added into with POETX_ACCUMULATE_GRAD in set->flags.  Sums over
+ *        tokens run in a fixed order in fp32.
+ */
+int poetx_adapters_backward(const poetx_adapters* set, const int32_t* seg_start, const int32_t* seg_adapter,
+                            int32_t nseg, const void* X, int64_t ldx, const void* dY, int64_t lddy, int64_t N,
+                            void* dX, int64_t lddx, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Optimizer steps over many tensors at once.  A set of tensors is described
  * once (poetx_param_table) and stepped with one launch per call, whatever the
  * number of tensors: the generators of every layer, adapters, any others.

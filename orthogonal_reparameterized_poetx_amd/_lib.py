@@ -35,6 +35,8 @@ EXPORTED = ("poetx_workspace_bytes", "poetx_build_workspace_bytes", "poetx_build
             "poetx_chain_workspace_bytes", "poetx_merge", "poetx_merge_blocks", "poetx_merge_blocks_sets",
             "poetx_merge_sets_workspace_bytes", "poetx_make_permutation",
             "poetx_adam_step", "poetx_w0_bytes", "poetx_quantize_w0", "poetx_dequantize_w0", "poetx_transpose_w0",
+            "poetx_adapter_table_bytes", "poetx_adapter_table", "poetx_adapters_workspace_bytes",
+            "poetx_adapters_forward", "poetx_adapters_backward",
             "poetx_param_table_bytes", "poetx_param_table", "poetx_grad_norm_workspace_bytes", "poetx_grad_norm",
             "poetx_adamw_step", "poetx_adamw_moments",
             "poetx_last_error", "poetx_timing_enable", "poetx_timing_summary")
@@ -71,6 +73,19 @@ class Blocks(ctypes.Structure):
     """poetx_blocks: prebuilt Cayley blocks of one layer."""
     _fields_ = [("Q32R", ctypes.c_void_p), ("Q32P", ctypes.c_void_p), ("QR", ctypes.c_void_p),
                 ("QP", ctypes.c_void_p), ("QTR", ctypes.c_void_p), ("QTP", ctypes.c_void_p)]
+
+
+class Adapter(ctypes.Structure):
+    """poetx_adapter: one low-rank adapter."""
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("dA", ctypes.c_void_p), ("dB", ctypes.c_void_p),
+                ("r", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Adapters(ctypes.Structure):
+    """poetx_adapters: filled by poetx_adapter_table."""
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32), ("count", ctypes.c_int32),
+                ("max_rank", ctypes.c_int32), ("flags", ctypes.c_uint32), ("layout", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("rows", ctypes.c_int64), ("table", ctypes.c_void_p)]
 
 
 class Param(ctypes.Structure):
@@ -165,6 +180,14 @@ def lib():
         "poetx_make_permutation": (ctypes.c_int, [u64, u64, i32, i64, vp]),
         "poetx_adam_step": (ctypes.c_int, [vp, vp, vp, vp, i64, i64, ctypes.c_float, ctypes.c_float,
                                            ctypes.c_float, ctypes.c_float, vp]),
+        "poetx_adapter_table_bytes": (sz, [i32]),
+        "poetx_adapter_table": (ctypes.c_int, [ctypes.POINTER(Adapter), i32, i64, i64, i32, vp, sz,
+                                               ctypes.POINTER(Adapters)]),
+        "poetx_adapters_workspace_bytes": (sz, [ctypes.POINTER(Adapters), i64, i32, ctypes.c_int]),
+        "poetx_adapters_forward": (ctypes.c_int, [ctypes.POINTER(Adapters), vp, vp, i32, vp, i64, i64, vp, i64, vp,
+                                                  sz, vp]),
+        "poetx_adapters_backward": (ctypes.c_int, [ctypes.POINTER(Adapters), vp, vp, i32, vp, i64, vp, i64, i64, vp,
+                                                   i64, vp, sz, vp]),
         "poetx_param_table_bytes": (sz, [ctypes.POINTER(Param), i32]),
         "poetx_param_table": (ctypes.c_int, [ctypes.POINTER(Param), i32, vp, sz, ctypes.POINTER(ParamSet)]),
         "poetx_grad_norm_workspace_bytes": (sz, [ctypes.POINTER(ParamSet)]),
@@ -408,6 +431,40 @@ def poetx_adam_step(theta, grad, m, v, count, step, lr=1e-3, beta1=0.9, beta2=0.
     _check("poetx_adam_step", lib().poetx_adam_step(_ptr(theta), _ptr(grad), _ptr(m), _ptr(v), int(count), int(step),
                                                     float(lr), float(beta1), float(beta2), float(eps),
                                                     _stream(stream)))
+
+
+def adapter_table(adapters, m, n, dtype):
+    """(host table as a uint8 tensor, Adapters without its table) of a sequence of Adapter."""
+    import torch
+    arr = (Adapter * max(len(adapters), 1))(*adapters)
+    need = lib().poetx_adapter_table_bytes(len(adapters))
+    if need == 0:
+        raise PoetxError("poetx_adapter_table_bytes", -2, last_error())
+    host = torch.zeros(need, dtype=torch.uint8)
+    out = Adapters()
+    _check("poetx_adapter_table", lib().poetx_adapter_table(arr, len(adapters), int(m), int(n), int(dtype),
+                                                            ctypes.c_void_p(host.data_ptr()), need,
+                                                            ctypes.byref(out)))
+    return host, out
+
+
+def adapters_workspace_bytes(aset, N, nseg, op):
+    n = lib().poetx_adapters_workspace_bytes(ctypes.byref(aset), int(N), int(nseg), int(op))
+    if n == 0:
+        raise PoetxError("poetx_adapters_workspace_bytes", -1, last_error())
+    return n
+
+
+def poetx_adapters_forward(aset, seg_start, seg_adapter, nseg, X, ldx, N, Y, ldy, ws, stream=None):
+    _check("poetx_adapters_forward", lib().poetx_adapters_forward(
+        ctypes.byref(aset), _ptr(seg_start), _ptr(seg_adapter), int(nseg), _ptr(X), int(ldx), int(N), _ptr(Y),
+        int(ldy), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def poetx_adapters_backward(aset, seg_start, seg_adapter, nseg, X, ldx, dY, lddy, N, dX, lddx, ws, stream=None):
+    _check("poetx_adapters_backward", lib().poetx_adapters_backward(
+        ctypes.byref(aset), _ptr(seg_start), _ptr(seg_adapter), int(nseg), _ptr(X), int(ldx), _ptr(dY), int(lddy),
+        int(N), _ptr(dX), int(lddx), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
 
 
 def param_table(params):
