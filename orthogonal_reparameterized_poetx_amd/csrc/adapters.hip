@@ -74,6 +74,15 @@ __device__ __forceinline__ AdTile find_tile(const AdSegs& g, int w) {
   }
 }
 
+// what an expand needs of a tile, written by the shrink before it
+struct AdInfo {
+  int32_t t0, rows;   // rows == 0: nothing to do
+  const void* W;      // rows of ldw: the adapter's B, or its part of At
+  int32_t ldw, pad[3];
+};
+
+template <int V> struct Int { static constexpr int value = V; };
+
 // ---- element types.  A fragment is 16 bytes of a row: EL elements; the four
 // lane groups of a wave hold KF = 4 EL elements of the contraction.  bf16: one
 // 16x16x32 MFMA; fp32: four 16x16x4 MFMAs, element e of every group in MFMA e.
@@ -94,111 +103,354 @@ template <> struct El<float> {
   }
 };
 
-// elements k .. k + EL of a row of `width`, zeros past its end
+// elements k .. k + EL of a row of `width`, zeros past its end.  VEC: rows of
+// whole 16-byte pieces.  Otherwise the piece may start at any element (global
+// loads of 16 bytes need no alignment beyond the element's) and is cut at the row's
+// end; `end` is the end of the matrix, past which nothing is read.
 template <typename E, bool VEC>
-__device__ __forceinline__ uint4 load_frag(const E* row, int k, int width) {
+__device__ __forceinline__ uint4 load_frag(const E* row, int k, int width, const E* end) {
   constexpr int EL = El<E>::EL;
-  if (VEC || k + EL <= width) {
-    if (VEC) return k < width ? ldg16(row + k) : make_uint4(0, 0, 0, 0);
-    E e[EL];
+  if (VEC) return k < width ? ldg16(row + k) : make_uint4(0, 0, 0, 0);
+  const int left = width - k;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (left <= 0) return v;
+  if (row + k + EL <= end) {
+    __builtin_memcpy(&v, row + k, 16);
+    if (left < EL) {
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < EL; ++i) e[i] = row[k + i];
-    return __builtin_bit_cast(uint4, e);
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (EL == 8) w[q] = left >= 2 * q + 2 ? w[q] : left == 2 * q + 1 ? w[q] & 0xffffu : 0u;
+        else w[q] = left > q ? w[q] : 0u;
+      }
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return v;
   }
   E e[EL];
 #pragma unroll
-  for (int i = 0; i < EL; ++i) e[i] = k + i < width ? row[k + i] : E(0);
+  for (int i = 0; i < EL; ++i) e[i] = i < left ? row[k + i] : E(0);
   return __builtin_bit_cast(uint4, e);
 }
 
-// ---- shrink: T[rank][token] of each tile, fp32 [rpmax][32]
+// ---- shrink: T of each tile, fp32, in one or both of two orders:
+//   rows   [rank][32 tokens], for the gradients
+//   frags  as the expand's lanes hold it: [step kk][half s][lane][EL], the value of
+//          rank kk KF + EL (lane / 16) + e and token 16 s + lane % 16 (bf16 sets of
+//          rank 16: [half][lane < 32][8])
+// A workgroup takes a tile, RT rank tiles and a part of the width; its eight
+// waves take every eighth step of 64 (fp32: 32) elements of that part, and add
+// their sums in LDS.  Each wave issues the loads of several steps before the
+// first product, so that one latency covers them.
 struct ShrinkJob {
   const void* X;      // [N][width], rows ldx apart
-  const void* W;      // null: each adapter's A; else the padded rows [row0 + rank][ldw]
-  float* T;
-  int64_t ldx, ldw;
+  float* rows;        // [tiles][rpmax * 32], nullable
+  float* frags;       // [parts][tiles][rpmax * 32], nullable
+  int64_t ldx;
   int width;
+  int useB;           // weights: each adapter's A [rank][width] or B [width][rank]
+};
+struct ListArgs {     // see build_list
+  int4* list;
+  int32_t* offs;
+  int cap;
+};
+struct TurnArgs {     // see turn_a
+  void* At;
+  int n, per, tw;     // per: workgroups of an adapter; tw: columns a workgroup turns
 };
 struct ShrinkArgs {
   ShrinkJob job[2];
   AdSegs seg;
   const AdEntry* table;
-  int rpmax;
+  AdInfo* info;       // of each tile, for the expand
+  ListArgs lists;     // extra workgroups after the tiles': count lists, then count * turn.per transposes
+  TurnArgs turn;
+  int rpmax, tiles, parts, groups;   // groups: rank groups of RT tiles; grid.y = jobs * groups * parts
 };
 
-template <typename E, int RT, bool VEC>
-__global__ __launch_bounds__(512) void adapter_shrink_kernel(const ShrinkArgs a) {
-  constexpr int EL = El<E>::EL, KF = El<E>::KF, WAVES = 8;
-  __shared__ float red[WAVES][512];
-  const int w = blockIdx.x;
-  const AdTile tile = find_tile(a.seg, w);
-  if (tile.rows == 0) return;
-  const ShrinkJob& J = a.job[blockIdx.y];
+// the tiles of each adapter, one adapter after another, for the gradients:
+// entry {t0, rows, adapter, tile index}; offs[a] the first entry of adapter a
+__device__ __forceinline__ int tiles_of(const AdSegs& g, int s, int& a, int& t0, int& t1) {
+  t0 = clamp_token(g.start[s], g.N);
+  t1 = clamp_token(g.start[s + 1], g.N);
+  a = g.which[s];
+  return a >= 0 && a < g.count && t1 > t0 ? (t1 - t0 + AD_T - 1) / AD_T : 0;
+}
+
+template <int THREADS>
+__device__ __forceinline__ void build_list(const AdSegs& g, const ListArgs& p, int me, int* cnt) {
+  constexpr int WAVES = THREADS / 64;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int before = 0;
+  for (int s = tid; s < g.nseg; s += THREADS) {
+    int a, t0, t1;
+    const int k = tiles_of(g, s, a, t0, t1);
+    if (k && a < me) before += k;
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) before += __shfl_xor(before, o);
+  if (lane == 0) cnt[wave] = before;
+  __syncthreads();
+  int pos = 0;
+  for (int q = 0; q < WAVES; ++q) pos += cnt[q];
+  __syncthreads();
+  // (segments that overlap, against the contract, could fill more than the list)
+  if (tid == 0) p.offs[me] = pos < p.cap ? pos : p.cap;
+  for (int s0 = 0; s0 < g.nseg; s0 += THREADS) {
+    int a = -1, t0 = 0, t1 = 0, k = 0;
+    if (s0 + tid < g.nseg) k = tiles_of(g, s0 + tid, a, t0, t1);
+    if (a != me) k = 0;
+    int inc = k;   // inclusive sum over the wave
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 63) cnt[wave] = inc;
+    __syncthreads();
+    int at = pos + inc - k;
+    for (int q = 0; q < wave; ++q) at += cnt[q];
+    for (int q = 0; q < WAVES; ++q) pos += cnt[q];
+    __syncthreads();
+    for (int i = 0; i < k; ++i) {
+      const int t = t0 + i * AD_T;
+      if (at + i < p.cap) p.list[at + i] = make_int4(t, t1 - t < AD_T ? t1 - t : AD_T, me, t0 / AD_T + s0 + tid + i);
+    }
+  }
+  if (tid == 0 && me == g.count - 1) p.offs[g.count] = pos < p.cap ? pos : p.cap;
+}
+
+__device__ __forceinline__ i16x4 ds_read_tr16a(const uint16_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(i16x4, const_cast<uint16_t*>(p)));
+}
+
+// At [column][rp] of each adapter, the ranks past r zero: with it dx is an expand
+template <typename E>
+__device__ __forceinline__ void turn_a(const AdEntry* table, const TurnArgs& p, int b, char* lds_raw) {
+  E* lds = reinterpret_cast<E*>(lds_raw);
+  const AdEntry ad = table[b / p.per];
+  const int tid = threadIdx.x, tw = p.tw, c0 = b % p.per * tw, cols = p.n - c0 < tw ? p.n - c0 : tw;
+  const int lane = tid & (tw - 1), row = tid / tw, rows = blockDim.x / tw;
+  const E* A = static_cast<const E*>(ad.A) + c0;
+  // a row of LDS: one column of A, its ranks; padded to an odd number of dwords
+  const int ld = ad.r + (sizeof(E) == 2 ? 2 + (ad.r & 1) : 1);
+  if (lane < cols)
+#pragma unroll 4
+    for (int r = row; r < ad.r; r += rows) lds[lane * ld + r] = A[(int64_t)r * p.n + lane];
+  __syncthreads();
+  E* out = static_cast<E*>(p.At) + (int64_t)ad.row0 * p.n + (int64_t)c0 * ad.rp;
+  const int total = cols * ad.rp;
+  int c = tid / ad.rp, r = tid % ad.rp;
+  const int dc = blockDim.x / ad.rp, dr = blockDim.x % ad.rp;
+  for (int i = tid; i < total; i += blockDim.x) {
+    out[i] = r < ad.r ? lds[c * ld + r] : E(0);
+    c += dc;
+    r += dr;
+    if (r >= ad.rp) { r -= ad.rp; ++c; }
+  }
+}
+
+constexpr int SHRINK_WAVES = 8;
+constexpr int TURN_LDS = 32 * 1024;   // bytes a transpose may take
+// LDS bytes of B's rows of one step for all waves (bf16), of the sums and of a transpose
+constexpr int shrink_lds(int rt, bool bf) {
+  const int stage = bf ? SHRINK_WAVES * 64 * 16 * rt * 2 : 0, red = SHRINK_WAVES * 512 * 4;
+  const int most = stage > red ? stage : red;
+  return most > TURN_LDS ? most : TURN_LDS;
+}
+
+template <typename E, int RT, bool VEC, bool USEB>
+__device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob& J, const AdTile& tile, int w,
+                                            int group, int part, char* lds) {
+  constexpr int EL = El<E>::EL, KF = El<E>::KF, STEP = 2 * KF;
+  constexpr bool STAGE = USEB && EL == 8;   // B's rows through LDS, read transposed
   const AdEntry ad = a.table[tile.adapter];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int rt_n = (ad.rp + 15) >> 4;
-  const E* X = static_cast<const E*>(J.X);
+  const int rank0 = group * RT * 16;
+  if (rank0 >= ad.rp) return;
+  const int rt_n = (ad.rp - rank0) >> 4;   // rank tiles of this adapter from rank0 on
   const E* x[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int t = 16 * s + l16;
-    x[s] = X + (int64_t)(tile.t0 + (t < tile.rows ? t : 0)) * J.ldx;
+    x[s] = static_cast<const E*>(J.X) + (int64_t)(tile.t0 + (t < tile.rows ? t : 0)) * J.ldx;
   }
-  const E* W = J.W ? static_cast<const E*>(J.W) + (int64_t)ad.row0 * J.ldw : static_cast<const E*>(ad.A);
-  const int64_t ldw = J.W ? J.ldw : J.width;
+  const E* xend = static_cast<const E*>(J.X) + (int64_t)(a.seg.N - 1) * J.ldx + J.width;
+  const E* W = static_cast<const E*>(USEB ? ad.B : ad.A);
+  const E* wend = W + (int64_t)ad.r * J.width;
+  uint16_t* stage = reinterpret_cast<uint16_t*>(lds) + wave * 64 * 16 * RT;
+  // staged rows hold the ranks rank0 .. rank0 + rw of B in rc pieces of eight
+  const int rw = ad.r - rank0 < 16 * RT ? ad.r - rank0 : 16 * RT, rc = (rw + 7) >> 3, ldst = rc * 8;
   f32x4 acc[RT][2];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // a step is two fragments: lane group g holds 2 EL neighbouring elements
-  for (int k0 = wave * 2 * KF; k0 < J.width; k0 += WAVES * 2 * KF) {
-    const int k = k0 + g * 2 * EL;
-    uint4 xf[2][2];
+
+  // UU steps from st on, every eighth; FULL: within the width
+  auto run = [&](auto uu, auto full, int st) {
+    constexpr int UU = decltype(uu)::value;
+    constexpr bool FULL = decltype(full)::value;
+    uint4 xf[UU][2][2], wf[UU][RT][2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int u = 0; u < UU; ++u) {
+      const int k0 = (st + u * SHRINK_WAVES) * STEP;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) xf[s][h] = load_frag<E, VEC>(x[s], k + h * EL, J.width);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      if (i < rt_n) {
-        const int rank = 16 * i + l16;
-        const E* wr = W + (int64_t)(rank < ad.r ? rank : 0) * ldw;
+      for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint4 wf = load_frag<E, VEC>(wr, k + h * EL, J.width);
-          acc[i][0] = El<E>::mma(wf, xf[0][h], acc[i][0]);
-          acc[i][1] = El<E>::mma(wf, xf[1][h], acc[i][1]);
+          const int k = k0 + h * KF + g * EL;   // fragment h of a step: element k0 + h KF + g EL + e
+          if (FULL && VEC) xf[u][s][h] = ldg16(x[s] + k);
+          else xf[u][s][h] = load_frag<E, VEC>(x[s], k, J.width, xend);
+        }
+      if constexpr (STAGE) {
+        // piece c of the step: row c / rc, ranks 8 (c % rc) on; 64 rows hold 64 rc pieces
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = (2 * i + h) * 64 + lane;
+            const int row = rc == 2 ? c >> 1 : rc == 4 ? c >> 2 : rc == 8 ? c >> 3 : c / rc;
+            const int j = k0 + row, cc = c - row * rc;
+            wf[u][i][h] = row < 64 && (FULL || j < J.width)
+                              ? load_frag<E, VEC>(W + (int64_t)j * ad.r + rank0, cc * 8, rw, wend)
+                              : make_uint4(0, 0, 0, 0);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const int rank = rank0 + 16 * i + l16, rr = rank < ad.r ? rank : 0;
+          if (i < rt_n) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int k = k0 + h * KF + g * EL;
+              if constexpr (USEB) {
+                E e[EL];
+#pragma unroll
+                for (int q = 0; q < EL; ++q) e[q] = k + q < J.width ? W[(int64_t)(k + q) * ad.r + rr] : E(0);
+                wf[u][i][h] = __builtin_bit_cast(uint4, e);
+              } else if (FULL && VEC) {
+                wf[u][i][h] = ldg16(W + (int64_t)rr * J.width + k);
+              } else {
+                wf[u][i][h] = load_frag<E, VEC>(W + (int64_t)rr * J.width, k, J.width, wend);
+              }
+            }
+          }
         }
       }
     }
+#pragma unroll
+    for (int u = 0; u < UU; ++u) {
+      if constexpr (STAGE) {
+        // LDS operations of a wave stay in order: the rows are in place before
+        // they are read, and read before the next step's are written
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = (2 * i + h) * 64 + lane;
+            if (c < 64 * rc) *reinterpret_cast<uint4*>(stage + c * 8) = wf[u][i][h];
+          }
+        asm volatile("" ::: "memory");
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        if (i < rt_n) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint4 f = wf[u][i][h];
+            if constexpr (STAGE) {
+              // 16 lanes read 4 rows of 16 ranks and get 4 rows of their own rank
+              // (past the staged pieces: another's, whose sums are dropped)
+              const int col = 16 * i + 4 * (l16 & 3) < ldst ? 16 * i + 4 * (l16 & 3) : 0;
+              const uint16_t* src = stage + (h * 32 + 8 * g + (l16 >> 2)) * ldst + col;
+              const i16x4 p = ds_read_tr16a(src), q = ds_read_tr16a(src + 4 * ldst);
+              typedef short i16x8 __attribute__((ext_vector_type(8)));
+              f = __builtin_bit_cast(uint4, i16x8{p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]});
+            }
+            acc[i][0] = El<E>::mma(f, xf[u][0][h], acc[i][0]);
+            acc[i][1] = El<E>::mma(f, xf[u][1][h], acc[i][1]);
+          }
+        }
+      }
+      if constexpr (STAGE) asm volatile("" ::: "memory");
+    }
+  };
+  // the part's whole steps, then (last part) the rest of the width
+  const int steps = J.width / STEP, per = (steps + a.parts - 1) / a.parts;
+  const int s_end = (part + 1) * per < steps ? (part + 1) * per : steps;
+  constexpr int U = RT == 1 ? 4 : 2;
+  int st = part * per + wave;
+  for (; st + (U - 1) * SHRINK_WAVES < s_end; st += U * SHRINK_WAVES) run(Int<U>{}, Int<1>{}, st);
+  if (U > 2 && st + SHRINK_WAVES < s_end) {
+    run(Int<2>{}, Int<1>{}, st);
+    st += 2 * SHRINK_WAVES;
   }
-  float* T = J.T + (int64_t)w * a.rpmax * AD_T;
+  if (st < s_end) run(Int<1>{}, Int<1>{}, st);
+  if (steps * STEP < J.width && part == a.parts - 1 && wave == SHRINK_WAVES - 1) run(Int<1>{}, Int<0>{}, steps);
+
+  float* red = reinterpret_cast<float*>(lds);
+  const int64_t size = (int64_t)a.rpmax * AD_T;
+  float* rows = J.rows ? J.rows + w * size : nullptr;
+  float* frags = J.frags ? J.frags + ((int64_t)part * a.tiles + w) * size : nullptr;
+  if (STAGE) __syncthreads();
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     if (i < rt_n) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) *reinterpret_cast<f32x4*>(&red[wave][s * 256 + lane * 4]) = acc[i][s];
+      for (int s = 0; s < 2; ++s) *reinterpret_cast<f32x4*>(&red[wave * 512 + s * 256 + lane * 4]) = acc[i][s];
       __syncthreads();
       float v = 0.f;
 #pragma unroll
-      for (int q = 0; q < WAVES; ++q) v += red[q][tid];
-      const int rank = 16 * i + 4 * ((tid >> 6) & 3) + (tid & 3), t = 16 * (tid >> 8) + ((tid >> 2) & 15);
-      T[rank * AD_T + t] = rank < ad.r && t < tile.rows ? v * ad.scale : 0.f;
+      for (int q = 0; q < SHRINK_WAVES; ++q) v += red[q * 512 + tid];
+      const int rank = rank0 + 16 * i + 4 * ((tid >> 6) & 3) + (tid & 3), s = tid >> 8, c = (tid >> 2) & 15;
+      const int t = 16 * s + c;
+      v = rank < ad.r && t < tile.rows ? v * ad.scale : 0.f;
+      if (rows) rows[rank * AD_T + t] = v;
+      if (frags) {
+        const int kk = rank / KF, gg = rank % KF / EL, e = rank % EL, lanes = a.rpmax < KF ? 16 * (a.rpmax / EL) : 64;
+        frags[((kk * 2 + s) * lanes + gg * 16 + c) * EL + e] = v;
+      }
       __syncthreads();
     }
   }
 }
 
-// ---- expand: Y[t][j] += sum_k T[k][t] W[j][k]
+template <typename E, int RT, bool VEC>
+__global__ __launch_bounds__(512) void adapter_shrink_kernel(const ShrinkArgs a) {
+  __shared__ __align__(16) char lds[shrink_lds(RT, sizeof(E) == 2)];
+  const int w = blockIdx.x;
+  if (w >= a.tiles) {
+    if (blockIdx.y) return;
+    if (w - a.tiles < a.seg.count) build_list<512>(a.seg, a.lists, w - a.tiles, reinterpret_cast<int*>(lds));
+    else turn_a<E>(a.table, a.turn, w - a.tiles - a.seg.count, lds);
+    return;
+  }
+  const AdTile tile = find_tile(a.seg, w);
+  if (blockIdx.y == 0 && threadIdx.x == 0) {
+    AdInfo in{tile.t0, tile.rows, nullptr, 0, {0, 0, 0}};
+    if (tile.rows) {
+      const AdEntry ad = a.table[tile.adapter];
+      in.W = a.turn.At ? static_cast<const E*>(a.turn.At) + (int64_t)ad.row0 * a.turn.n : static_cast<const E*>(ad.B);
+      in.ldw = a.turn.At ? ad.rp : ad.r;
+    }
+    a.info[w] = in;
+  }
+  if (tile.rows == 0) return;
+  const int part = blockIdx.y % a.parts, group = blockIdx.y / a.parts % a.groups;
+  const ShrinkJob& J = a.job[blockIdx.y / (a.parts * a.groups)];
+  if (J.useB) shrink_body<E, RT, VEC, true>(a, J, tile, w, group, part, lds);
+  else shrink_body<E, RT, VEC, false>(a, J, tile, w, group, part, lds);
+}
+
+// ---- expand: Y[t][j] += sum_k T[k][t] W[j][k], W = each adapter's B, or (dx) At
 struct ExpandArgs {
   void* Y;
   int64_t ldy;
-  int width, cols;      // cols: columns of a workgroup
-  const void* W;        // null: each adapter's B (rows of r); else the padded rows, adapter a's from row0 * width on, rows of rp
-  const float* T;
-  AdSegs seg;
-  const AdEntry* table;
-  int rpmax;
+  int width;
+  const float* T;       // frags [parts][tiles][rpmax * 32], the parts to be added
+  const AdInfo* info;
+  int rpmax, tiles, parts;
 };
 
 // 8 (bf16) fp32 values as bf16 pairs: hi, and lo = value - hi, which keep 16 bits of the value
@@ -215,6 +467,49 @@ __device__ __forceinline__ void split8(const float f[8], uint4& hi, uint4& lo) {
   lo = as_u4(l);
 }
 
+// the lanes' 8 rows of 8 bf16 (x[i]: row i) as 8 operands of 8 rows (op[e]: column e)
+__device__ __forceinline__ void transpose8(const uint4 x[8], uint4 op[8]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t d[8], lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = c == 0 ? x[i].x : c == 1 ? x[i].y : c == 2 ? x[i].z : x[i].w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = __builtin_amdgcn_perm(d[2 * i + 1], d[2 * i], 0x05040100u);
+      hi[i] = __builtin_amdgcn_perm(d[2 * i + 1], d[2 * i], 0x07060302u);
+    }
+    op[2 * c] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    op[2 * c + 1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  }
+}
+
+// y + v for EL elements
+template <typename E>
+__device__ __forceinline__ uint4 add_frag(uint4 y, const float* v) {
+  const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+  uint32_t n[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (sizeof(E) == 2)
+      n[q] = pack2(f32_to_bits(__uint_as_float(w[q] << 16) + v[2 * q]),
+                   f32_to_bits(__uint_as_float(w[q] & 0xffff0000u) + v[2 * q + 1]));
+    else
+      n[q] = __float_as_uint(__uint_as_float(w[q]) + v[q]);
+  }
+  return make_uint4(n[0], n[1], n[2], n[3]);
+}
+
+// A workgroup takes one tile and 256 columns, 64 a wave; column groups of a tile
+// follow one another in the grid.  Small workgroups in the order of the memory
+// are what in-place updates of Y want: the same kernel with runs of four tiles
+// a workgroup, W kept in registers and the next tile's Y fetched ahead
+// took 48 us where this order takes 3X us (8192 x 5632, rank 16).
+// The MFMA's rows are the wave's columns, in an order that gives each lane EL
+// neighbouring columns of a token, and the four lanes of a token neighbouring
+// 16-byte pieces.
+constexpr int EXPAND_Y = 32768;   // tiles along the grid's second dimension
+
 template <typename E, int RT, bool VECY, bool VECW>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a) {
   constexpr int EL = El<E>::EL, KF = El<E>::KF;
@@ -222,195 +517,121 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a)
   constexpr bool PACK = BF && RT == 1;   // 16 ranks: hi and lo side by side in one MFMA
   constexpr int NK = PACK ? 1 : RT * 16 / KF;
   constexpr int NP = BF && !PACK ? 2 : 1;
-  const AdTile tile = find_tile(a.seg, blockIdx.x);
-  if (tile.rows == 0) return;
-  const AdEntry ad = a.table[tile.adapter];
+  constexpr int NH = 16 / EL;            // 16-byte pieces of a lane and token
+  constexpr int CP = EL / 4;             // MFMAs of a piece
+  constexpr int KU = RT <= 4 ? NK : 1;   // contraction steps whose operands are in flight together
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const float* T = a.T + (int64_t)blockIdx.x * a.rpmax * AD_T;
-  const int nk = PACK ? 1 : ad.rp / KF;
-  // column of fragment c, element k: kk * KF + kc + e
+  const int jb = blockIdx.x * 256 + wave * 64;
+  const int64_t w = (int64_t)blockIdx.z * EXPAND_Y + blockIdx.y;
+  if (jb >= a.width || w >= a.tiles) return;
+  const AdInfo in = a.info[w];
+  // element e of contraction step kk: rank kk KF + kc + e
   const int kc = PACK ? 8 * (g & 1) : g * EL;
-  uint4 tf[NK][2][NP];
+  const int64_t size = (int64_t)a.rpmax * AD_T;
+  const float* T = a.T + w * size + (PACK ? (lane & 31) : lane) * EL;
+  constexpr int TS = PACK ? 32 * EL : 64 * EL;   // floats of one half of a step
+  if (in.rows == 0) return;
+  const E* W = static_cast<const E*>(in.W);
+  const E* wend = W + (int64_t)a.width * in.ldw;
+  E* y[2];
 #pragma unroll
-  for (int kk = 0; kk < NK; ++kk) {
+  for (int s = 0; s < 2; ++s) y[s] = static_cast<E*>(a.Y) + (int64_t)(in.t0 + 16 * s + l16) * a.ldy + jb + g * EL;
+  const int left = a.width - jb - g * EL;   // columns from the lane's first on
+  uint4 yv[2][NH];
+  if (VECY) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      float f[8];
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int e = 0; e < EL; ++e) f[e] = kk >= nk ? 0.f : T[(kk * KF + kc + e) * AD_T + 16 * s + l16];
-      if constexpr (BF) {
-        uint4 hi, lo;
-        split8(f, hi, lo);
-        if constexpr (PACK) {
-          const bool first = g < 2;
-          tf[kk][s][0] = make_uint4(first ? hi.x : lo.x, first ? hi.y : lo.y, first ? hi.z : lo.z, first ? hi.w : lo.w);
-        } else {
-          tf[kk][s][0] = hi;
-          tf[kk][s][NP - 1] = lo;
-        }
-      } else {
-        tf[kk][s][0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                  __float_as_uint(f[3]));
-      }
-    }
+      for (int h = 0; h < NH; ++h)
+        if (h * 4 * EL < left && 16 * s + l16 < in.rows) yv[s][h] = ldg16(y[s] + h * 4 * EL);
   }
-  const E* W = a.W ? static_cast<const E*>(a.W) + (int64_t)ad.row0 * a.width : static_cast<const E*>(ad.B);
-  const int ldw = a.W ? ad.rp : ad.r;
-  const int c0 = blockIdx.y * a.cols, c1 = c0 + a.cols < a.width ? c0 + a.cols : a.width;
-  for (int jb = c0 + wave * 64; jb < c1; jb += 256) {
-    // row of MFMA c, index 4 g' + q, is column jb + 16 g' + 4 c + q: a lane then holds 16 neighbouring columns
-    f32x4 acc[4][2];
+  f32x4 acc[4][2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      acc[c][0] = acc[c][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      int j = jb + 16 * (l16 >> 2) + 4 * c + (l16 & 3);
-      j = j < a.width ? j : a.width - 1;
-      const E* wr = W + (int64_t)j * ldw;
+  for (int c = 0; c < 4; ++c) acc[c][0] = acc[c][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int k0 = 0; k0 < NK; k0 += KU) {
+    if (k0 > 0 && k0 * KF >= in.ldw) break;
+    uint4 wf[KU][4];
+    f32x4 t[KU][2][CP];
 #pragma unroll
-      for (int kk = 0; kk < NK; ++kk) {
-        if (kk < nk) {
-          const uint4 wf = load_frag<E, VECW>(wr, kk * KF + kc, ldw);
+    for (int u = 0; u < KU; ++u) {
+      const int kk = k0 + u;
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int p = 0; p < NP; ++p) acc[c][s] = El<E>::mma(wf, tf[kk][s][p], acc[c][s]);
-        }
+      for (int c = 0; c < 4; ++c) {
+        int j = jb + (c / CP) * 4 * EL + (l16 >> 2) * EL + 4 * (c % CP) + (l16 & 3);
+        j = j < a.width ? j : a.width - 1;
+        wf[u][c] = load_frag<E, VECW>(W + (int64_t)j * in.ldw, kk * KF + kc, in.ldw, wend);
       }
+      // (steps past the adapter's ranks: W is zero, T another's or none)
+      const bool tin = kk * KF < in.ldw;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int q = 0; q < CP; ++q)
+          t[u][s][q] = tin ? *reinterpret_cast<const f32x4*>(T + (kk * 2 + s) * TS + 4 * q) : f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int p = 1; p < a.parts; ++p)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int q = 0; q < CP; ++q)
+            if (tin) t[u][s][q] += *reinterpret_cast<const f32x4*>(T + p * a.tiles * size + (kk * 2 + s) * TS + 4 * q);
     }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int t = 16 * s + l16;
-      if (t >= tile.rows) continue;
-      E* y = static_cast<E*>(a.Y) + (int64_t)(tile.t0 + t) * a.ldy;
-      const int j0 = jb + 16 * g;
+    for (int u = 0; u < KU; ++u) {
+      uint4 tf[2][NP];
 #pragma unroll
-      for (int h = 0; h < 16 / EL; ++h) {
-        const int j = j0 + h * EL;
-        float v[EL];
+      for (int s = 0; s < 2; ++s) {
+        if constexpr (BF) {
+          float f[8];
 #pragma unroll
-        for (int e = 0; e < EL; ++e) v[e] = acc[(h * EL + e) >> 2][s][e & 3];
-        if (VECY) {
-          if (j >= a.width) continue;
-          const uint4 o = ldg16(y + j);
-          const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
-          uint32_t n[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if constexpr (BF)
-              n[q] = pack2(f32_to_bits(__uint_as_float(ow[q] << 16) + v[2 * q]),
-                           f32_to_bits(__uint_as_float(ow[q] & 0xffff0000u) + v[2 * q + 1]));
-            else
-              n[q] = __float_as_uint(__uint_as_float(ow[q]) + v[q]);
+          for (int e = 0; e < 8; ++e) f[e] = t[u][s][e >> 2][e & 3];
+          uint4 hi, lo;
+          split8(f, hi, lo);
+          if constexpr (PACK) {
+            const bool first = g < 2;
+            tf[s][0] = make_uint4(first ? hi.x : lo.x, first ? hi.y : lo.y, first ? hi.z : lo.z, first ? hi.w : lo.w);
+          } else {
+            tf[s][0] = hi;
+            tf[s][NP - 1] = lo;
           }
-          stg16(y + j, make_uint4(n[0], n[1], n[2], n[3]));
         } else {
-#pragma unroll
-          for (int e = 0; e < EL; ++e)
-            if (j + e < a.width) {
-              if constexpr (BF) y[j + e] = f32_to_bits(bits_to_f32(y[j + e]) + v[e]);
-              else y[j + e] += v[e];
-            }
+          tf[s][0] = __builtin_bit_cast(uint4, t[u][s][0]);
         }
       }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) acc[c][s] = El<E>::mma(wf[u][c], tf[s][p], acc[c][s]);
     }
   }
-}
-
-// ---- the tiles of each adapter, one adapter after another, for the gradients:
-// list entry {t0, rows, adapter, tile index}, offs[a] the first entry of
-// adapter a; and the transposed, rank-padded adapters: Bt [rank][mp] and
-// At [column][rp], which make U a shrink and dx an expand.
-struct PrepArgs {
-  AdSegs seg;
-  const AdEntry* table;
-  int4* list;
-  int32_t* offs;
-  void *Bt, *At;
-  int m, n, mp, cap, tw;   // cap: entries of list; tw: rows of B or columns of A a transpose takes at a time
-};
-
-__device__ __forceinline__ int tiles_of(const AdSegs& g, int s, int& a, int& t0, int& t1) {
-  t0 = clamp_token(g.start[s], g.N);
-  t1 = clamp_token(g.start[s + 1], g.N);
-  a = g.which[s];
-  return a >= 0 && a < g.count && t1 > t0 ? (t1 - t0 + AD_T - 1) / AD_T : 0;
-}
-
-template <typename E>
-__global__ __launch_bounds__(256) void adapter_prep_kernel(const PrepArgs p) {
-  extern __shared__ char lds_raw[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if ((int)blockIdx.x < p.seg.count) {
-    int* cnt = reinterpret_cast<int*>(lds_raw);   // [4] sums of the waves
-    const int me = blockIdx.x;
-    int before = 0;
-    for (int s = tid; s < p.seg.nseg; s += 256) {
-      int a, t0, t1;
-      const int k = tiles_of(p.seg, s, a, t0, t1);
-      if (k && a < me) before += k;
-    }
 #pragma unroll
-    for (int o = 32; o; o >>= 1) before += __shfl_xor(before, o);
-    if (lane == 0) cnt[wave] = before;
-    __syncthreads();
-    int pos = cnt[0] + cnt[1] + cnt[2] + cnt[3];
-    __syncthreads();
-    // (segments that overlap, against the contract, could fill more than the list)
-    if (tid == 0) p.offs[me] = pos < p.cap ? pos : p.cap;
-    for (int s0 = 0; s0 < p.seg.nseg; s0 += 256) {
-      int a = -1, t0 = 0, t1 = 0, k = 0;
-      if (s0 + tid < p.seg.nseg) k = tiles_of(p.seg, s0 + tid, a, t0, t1);
-      if (a != me) k = 0;
-      int inc = k;   // inclusive sum over the wave
+  for (int s = 0; s < 2; ++s) {
+    if (16 * s + l16 >= in.rows) continue;
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int y = __shfl_up(inc, o);
-        if (lane >= o) inc += y;
+    for (int h = 0; h < NH; ++h) {
+      E* o = y[s] + h * 4 * EL;
+      const int n = left - h * 4 * EL;
+      float v[EL];
+#pragma unroll
+      for (int e = 0; e < EL; ++e) v[e] = acc[h * CP + (e >> 2)][s][e & 3];
+      if (VECY) {
+        if (n > 0) stg16(o, add_frag<E>(yv[s][h], v));
+      } else if (n >= EL) {
+        uint4 x;
+        __builtin_memcpy(&x, o, 16);
+        x = add_frag<E>(x, v);
+        __builtin_memcpy(o, &x, 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < EL; ++e)
+          if (e < n) {
+            if constexpr (BF) o[e] = f32_to_bits(bits_to_f32(o[e]) + v[e]);
+            else o[e] += v[e];
+          }
       }
-      if (lane == 63) cnt[wave] = inc;
-      __syncthreads();
-      int at = pos + inc - k;
-      for (int q = 0; q < wave; ++q) at += cnt[q];
-      pos += cnt[0] + cnt[1] + cnt[2] + cnt[3];
-      __syncthreads();
-      for (int i = 0; i < k; ++i) {
-        const int t = t0 + i * AD_T;
-        if (at + i < p.cap) p.list[at + i] = make_int4(t, t1 - t < AD_T ? t1 - t : AD_T, me, t0 / AD_T + s0 + tid + i);
-      }
-    }
-    if (tid == 0 && me == p.seg.count - 1) p.offs[p.seg.count] = pos < p.cap ? pos : p.cap;
-    return;
-  }
-  // transposes
-  E* lds = reinterpret_cast<E*>(lds_raw);
-  const int tw = p.tw, bt = (p.m + tw - 1) / tw, at = (p.n + tw - 1) / tw;
-  int b = blockIdx.x - p.seg.count;
-  const AdEntry ad = p.table[b / (bt + at)];
-  b %= bt + at;
-  if (b < bt) {
-    const int j0 = b * tw, rows = p.m - j0 < tw ? p.m - j0 : tw;
-    const E* B = static_cast<const E*>(ad.B) + (int64_t)j0 * ad.r;
-    for (int i = tid; i < rows * ad.r; i += 256) lds[(i / ad.r) * (ad.r + 1) + i % ad.r] = B[i];
-    __syncthreads();
-    E* out = static_cast<E*>(p.Bt) + (int64_t)ad.row0 * p.mp + j0;
-    const int cols = p.mp - j0 < tw ? p.mp - j0 : tw;
-    for (int i = tid; i < ad.rp * tw; i += 256) {
-      const int rank = i / tw, j = i % tw;
-      if (j < cols) out[(int64_t)rank * p.mp + j] = rank < ad.r && j < rows ? lds[j * (ad.r + 1) + rank] : E(0);
-    }
-  } else {
-    const int i0 = (b - bt) * tw, cols = p.n - i0 < tw ? p.n - i0 : tw;
-    const E* A = static_cast<const E*>(ad.A) + i0;
-    for (int i = tid; i < ad.r * tw; i += 256) {
-      const int rank = i / tw, c = i % tw;
-      if (c < cols) lds[c * (ad.r + 1) + rank] = A[(int64_t)rank * p.n + c];
-    }
-    __syncthreads();
-    E* out = static_cast<E*>(p.At) + (int64_t)ad.row0 * p.n + (int64_t)i0 * ad.rp;
-    for (int i = tid; i < cols * ad.rp; i += 256) {
-      const int c = i / ad.rp, rank = i % ad.rp;
-      out[i] = rank < ad.r ? lds[c * (ad.r + 1) + rank] : E(0);
     }
   }
 }
@@ -428,6 +649,7 @@ struct OuterArgs {
   const int4* list;
   const int32_t* offs;
   int count, rpmax, run, groups;   // run: list entries of a workgroup; groups of 64 ranks
+  int N;
 };
 
 // Wave: one slab of columns (16 lanes x EL), every list entry of the run.
@@ -484,54 +706,51 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
       }
     }
   };
-  clear();
-  int cur = -1;
-  for (int p = e0; p < e1; ++p) {
-    const int4 en = a.list[p];
-    if (en.z != cur) {
-      if (cur >= 0) {
-        flush(cur);
-        clear();
-      }
-      cur = en.z;
-    }
+  const E* xend = static_cast<const E*>(J.X) + (int64_t)(a.N - 1) * J.ldx + J.width;
+  auto load = [&](uint4 (&x)[8], const int4& en) {
     const E* X = static_cast<const E*>(J.X) + (int64_t)en.x * J.ldx;
-    const float* T = J.T + (int64_t)en.w * a.rpmax * AD_T;
-    uint4 x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int t = BF ? 8 * g + i : 4 * i + g;
       // past the tile's end T is zero, but 0 x NaN is not
-      x[i] = t < en.y ? load_frag<E, VEC>(X + (int64_t)t * J.ldx, col, J.width) : make_uint4(0, 0, 0, 0);
+      x[i] = t < en.y ? load_frag<E, VEC>(X + (int64_t)t * J.ldx, col, J.width, xend) : make_uint4(0, 0, 0, 0);
     }
+  };
+  clear();
+  int4 en = a.list[e0];
+  int cur = en.z;
+  uint4 x[8], nx[8];
+  load(x, en);
+  for (int p = e0;;) {
+    const bool more = p + 1 < e1;
+    int4 en2 = en;
+    if (more) {
+      en2 = a.list[p + 1];
+      load(nx, en2);   // on its way while this tile is multiplied
+    }
+    const float* T = J.T + (int64_t)en.w * a.rpmax * AD_T;
     if constexpr (BF) {
       uint4 op[8];   // operand e: column e of the lane, eight tokens
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t d[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = c == 0 ? x[i].x : c == 1 ? x[i].y : c == 2 ? x[i].z : x[i].w;
-        uint32_t lo[4], hi[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          lo[i] = __builtin_amdgcn_perm(d[2 * i + 1], d[2 * i], 0x05040100u);
-          hi[i] = __builtin_amdgcn_perm(d[2 * i + 1], d[2 * i], 0x07060302u);
-        }
-        op[2 * c] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        op[2 * c + 1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      }
+      transpose8(x, op);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         const int rank = grp * 64 + 16 * i + l16;
         const float* tr = T + (rank < a.rpmax ? rank : 0) * AD_T + 8 * g;
         const f32x4 f0 = *reinterpret_cast<const f32x4*>(tr), f1 = *reinterpret_cast<const f32x4*>(tr + 4);
         const float f[8] = {f0[0], f0[1], f0[2], f0[3], f1[0], f1[1], f1[2], f1[3]};
-        uint4 h, l;
+        // three bf16 values keep all 24 bits of T: the gradients are fp32
+        float rest[8];
+        uint4 h, l, l2, none;
         split8(f, h, l);
+        const bf16x8 hb = as_bf16x8(h), lb = as_bf16x8(l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rest[e] = f[e] - (float)hb[e] - (float)lb[e];
+        split8(rest, l2, none);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           acc[e][i] = El<E>::mma(op[e], h, acc[e][i]);
           acc[e][i] = El<E>::mma(op[e], l, acc[e][i]);
+          acc[e][i] = El<E>::mma(op[e], l2, acc[e][i]);
         }
       }
     } else {
@@ -549,6 +768,16 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
         }
       }
     }
+    if (!more) break;
+    if (en2.z != cur) {
+      flush(cur);
+      clear();
+      cur = en2.z;
+    }
+    ++p;
+    en = en2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = nx[i];
   }
   flush(cur);
 }
@@ -561,23 +790,54 @@ struct ReduceArgs {
   int rpmax, run, accumulate;
 };
 
-// dA [r][n] and dB [m][r] of every adapter; zero where it had no token
+// dA [r][n] and dB [m][r] of every adapter; zero where it had no token.  A
+// workgroup takes 64 columns and 16 ranks; dB turns through LDS.
 __global__ __launch_bounds__(256) void adapter_reduce_kernel(const ReduceArgs a) {
-  const int ad = blockIdx.y, job = blockIdx.z, width = a.width[job];
+  __shared__ float turn[64][17];
+  const int ad = blockIdx.y, job = blockIdx.z & 1, rank0 = (blockIdx.z >> 1) * 16, width = a.width[job];
   const AdEntry e = a.table[ad];
   float* out = job ? e.dB : e.dA;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (!out || i >= (int64_t)e.r * width) return;
-  const int rank = (int)(i / width), col = (int)(i % width);
+  const int col = blockIdx.x * 64 + (threadIdx.x & 63);
+  if (!out || rank0 >= e.r || (int)blockIdx.x * 64 >= width) return;
   const int o0 = a.offs[ad], o1 = a.offs[ad + 1];
-  float v = 0.f;
-  if (o1 > o0) {
-    const int q1 = (o1 - 1) / a.run;
-    const float* p = a.part[job] + (int64_t)rank * width + col;
-    for (int q = o0 / a.run; q <= q1; ++q) v += p[(int64_t)(q + ad) * a.rpmax * width];
+  const int q0 = o0 / a.run, q1 = o1 > o0 ? (o1 - 1) / a.run : q0 - 1;
+  const int64_t stride = (int64_t)a.rpmax * width;
+  const int rank = rank0 + (threadIdx.x >> 6) * 4;   // four ranks a thread
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (col < width) {
+    const float* p = a.part[job] + (q0 + ad) * stride + (int64_t)rank * width + col;
+#pragma unroll 4
+    for (int q = q0; q <= q1; ++q, p += stride)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += p[i * width];   // (ranks past r: padding of the slot)
   }
-  float* dst = job ? out + (int64_t)col * e.r + rank : out + i;
-  *dst = a.accumulate ? *dst + v : v;
+  if (job == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (rank + i < e.r && col < width) {
+        float* dst = out + (int64_t)(rank + i) * width + col;
+        *dst = a.accumulate ? *dst + v[i] : v[i];
+      }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) turn[threadIdx.x & 63][rank - rank0 + i] = v[i];
+  __syncthreads();
+  const int ranks = e.r - rank0 < 16 ? e.r - rank0 : 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = threadIdx.x + 256 * i, c = k >> 4, rr = k & 15;
+    const int j = blockIdx.x * 64 + c;
+    if (rr < ranks && j < width) {
+      float* dst = out + (int64_t)j * e.r + rank0 + rr;
+      *dst = a.accumulate ? *dst + turn[c][rr] : turn[c][rr];
+    }
+  }
+}
+
+__global__ __launch_bounds__(512) void adapter_list_kernel(const AdSegs seg, const ListArgs lists) {
+  __shared__ int cnt[8];
+  build_list<512>(seg, lists, blockIdx.x, cnt);
 }
 
 }  // namespace poetx
@@ -592,10 +852,6 @@ enum { LAY_A16 = 1, LAY_B16 = 2 };   // poetx_adapters.layout
 
 // ranks in whole MFMA steps: 16, or multiples of 32 for all adapters of a set with a rank over 16
 int pad_rank(int r, int rmax) { return rmax <= 16 ? 16 : (r + 31) / 32 * 32; }
-int rank_tiles(int rmax) {
-  const int rp = pad_rank(rmax, rmax);
-  return rp <= 16 ? 1 : rp <= 32 ? 2 : rp <= 64 ? 4 : rp <= 128 ? 8 : 16;
-}
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int check_dims(int64_t m, int64_t n, int32_t dtype) {
@@ -638,20 +894,34 @@ int check_rows(const char* name, const void* p, int64_t ld, int64_t width, int32
 
 struct AdPlan {
   int64_t tiles;           // tile indices of a call
-  int rpmax, mp, run, runs, slots, groups;
-  float *T, *U, *part[2];
-  void *Bt, *At;
+  int rpmax, run, runs, slots, groups;
+  int rt, rgroups, parts;  // shrink: rank tiles of a workgroup, their groups, parts of the width
+  float *T, *U, *F, *part[2];   // rows of T and U; frags of the expand's operand
+  void* At;
+  AdInfo* info;
   int4* list;
   int32_t* offs;
   size_t bytes;
 };
 
+int ceil_rt(int t) { return t <= 1 ? 1 : t <= 2 ? 2 : t <= 4 ? 4 : t <= 8 ? 8 : 16; }
+
 AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd, void* ws) {
   AdPlan p{};
   const bool f32 = s->dtype == POETX_F32;
-  const size_t es = f32 ? 4 : 2;
   p.tiles = N / AD_T + nseg;
   p.rpmax = pad_rank(s->max_rank, s->max_rank);
+  // few tiles: the ranks, then (forward) the width, are shared out over more workgroups
+  const int rt_all = p.rpmax / 16;
+  p.rt = rt_all < 4 ? ceil_rt(rt_all) : 4;
+  auto groups = [&](int rt) { return (rt_all + rt - 1) / rt; };
+  while (p.rt > 1 && p.tiles * (bwd ? 2 : 1) * groups(p.rt) < 512) p.rt /= 2;
+  p.rgroups = groups(p.rt);
+  p.parts = 1;
+  if (!bwd) {
+    const int64_t steps = (s->n + (f32 ? 31 : 63)) / (f32 ? 32 : 64);
+    while (p.parts < 8 && p.tiles * p.rgroups * p.parts < 256 && steps >= 16 * p.parts) p.parts *= 2;
+  }
   size_t off = 0;
   auto take = [&](size_t bytes) -> char* {
     off = (off + kWsAlign - 1) / kWsAlign * kWsAlign;
@@ -660,19 +930,19 @@ AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd,
     return q;
   };
   const size_t tbytes = (size_t)p.tiles * p.rpmax * AD_T * sizeof(float);
-  p.T = reinterpret_cast<float*>(take(tbytes));
+  p.info = reinterpret_cast<AdInfo*>(take((size_t)p.tiles * sizeof(AdInfo)));
+  p.F = reinterpret_cast<float*>(take(p.parts * tbytes));
   if (bwd) {
+    p.T = reinterpret_cast<float*>(take(tbytes));
     p.U = reinterpret_cast<float*>(take(tbytes));
-    p.mp = (int)((s->m + 7) / 8 * 8);
-    p.Bt = take((size_t)s->rows * p.mp * es);
-    p.At = take((size_t)s->rows * s->n * es);
+    p.At = take((size_t)s->rows * s->n * (f32 ? 4 : 2));
     p.list = reinterpret_cast<int4*>(take((size_t)p.tiles * sizeof(int4)));
     p.offs = reinterpret_cast<int32_t*>(take((size_t)(s->count + 1) * sizeof(int32_t)));
-    // runs of tiles: about 1024 workgroups over both gradients
+    // runs of tiles: about 512 workgroups over both gradients
     p.groups = (p.rpmax + 63) / 64;
     const int64_t slab = 4 * 16 * (f32 ? 4 : 8);
     const int64_t x = ((s->m + slab - 1) / slab + (s->n + slab - 1) / slab) * p.groups;
-    int64_t runs = 1024 / x;
+    int64_t runs = 512 / x;
     if (runs < 1) runs = 1;
     if (runs > p.tiles) runs = p.tiles > 0 ? p.tiles : 1;
     p.run = (int)((p.tiles + runs - 1) / runs);
@@ -690,14 +960,19 @@ AdSegs segs_of(const poetx_adapters* s, const int32_t* start, const int32_t* whi
   return AdSegs{start, which, nseg, s->count, (int32_t)N};
 }
 
-template <typename E, int RT, bool VEC>
-void shrink(const ShrinkArgs& a, int64_t tiles, int jobs, hipStream_t s) {
-  hipLaunchKernelGGL((adapter_shrink_kernel<E, RT, VEC>), dim3((unsigned)tiles, jobs), dim3(512), 0, s, a);
-}
 template <typename E>
-void launch_shrink(const ShrinkArgs& a, int64_t tiles, int jobs, int rt, bool vec, hipStream_t s) {
-#define POETX_RT(R) case R: vec ? shrink<E, R, true>(a, tiles, jobs, s) : shrink<E, R, false>(a, tiles, jobs, s); break;
-  switch (rt) { POETX_RT(1) POETX_RT(2) POETX_RT(4) POETX_RT(8) POETX_RT(16) }
+void launch_shrink(ShrinkArgs a, const AdPlan& p, int jobs, int extra, bool vec, hipStream_t s) {
+  a.rpmax = p.rpmax;
+  a.tiles = (int)p.tiles;
+  a.parts = p.parts;
+  a.groups = p.rgroups;
+  const dim3 grid((unsigned)(p.tiles + extra), (unsigned)(jobs * p.rgroups * p.parts));
+#define POETX_RT(R) \
+  case R: \
+    if (vec) hipLaunchKernelGGL((adapter_shrink_kernel<E, R, true>), grid, dim3(512), 0, s, a); \
+    else hipLaunchKernelGGL((adapter_shrink_kernel<E, R, false>), grid, dim3(512), 0, s, a); \
+    break;
+  switch (p.rt) { POETX_RT(1) POETX_RT(2) POETX_RT(4) }
 #undef POETX_RT
 }
 
@@ -705,20 +980,20 @@ template <typename E, int RT>
 void expand(const ExpandArgs& a, dim3 grid, bool vecy, bool vecw, hipStream_t s) {
   if (vecy && vecw) hipLaunchKernelGGL((adapter_expand_kernel<E, RT, true, true>), grid, dim3(256), 0, s, a);
   else if (vecy) hipLaunchKernelGGL((adapter_expand_kernel<E, RT, true, false>), grid, dim3(256), 0, s, a);
-  else if (vecw) hipLaunchKernelGGL((adapter_expand_kernel<E, RT, false, true>), grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((adapter_expand_kernel<E, RT, false, false>), grid, dim3(256), 0, s, a);
 }
 template <typename E>
-void launch_expand(ExpandArgs a, int64_t tiles, int rt, bool vecw, hipStream_t s) {
+void launch_expand(ExpandArgs a, const AdPlan& p, bool vecw, hipStream_t s) {
   const size_t es = sizeof(E);
   const bool vecy = al16(a.Y) && a.ldy * es % 16 == 0 && a.width * es % 16 == 0;
-  // columns of a workgroup: enough workgroups to fill the chip, then as many columns as there are
-  int64_t parts = (2048 + tiles - 1) / tiles;
-  const int64_t most = (a.width + 255) / 256;
-  if (parts > most) parts = most;
-  a.cols = (int)((most + parts - 1) / parts * 256);
-  const dim3 grid((unsigned)tiles, (unsigned)((a.width + a.cols - 1) / a.cols));
-  switch (rt) {
+  a.T = p.F;
+  a.info = p.info;
+  a.rpmax = p.rpmax;
+  a.tiles = (int)p.tiles;
+  a.parts = p.parts;
+  const dim3 grid((unsigned)((a.width + 255) / 256), (unsigned)(p.tiles < EXPAND_Y ? p.tiles : EXPAND_Y),
+                  (unsigned)((p.tiles + EXPAND_Y - 1) / EXPAND_Y));
+  switch (ceil_rt(p.rpmax / 16)) {
     case 1: expand<E, 1>(a, grid, vecy, vecw, s); break;
     case 2: expand<E, 2>(a, grid, vecy, vecw, s); break;
     case 4: expand<E, 4>(a, grid, vecy, vecw, s); break;
@@ -737,24 +1012,23 @@ template <typename E>
 int forward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, int64_t ldx, void* Y, int64_t ldy,
                  const AdPlan& p, hipStream_t s) {
   const size_t es = sizeof(E);
-  const int rt = rank_tiles(set->max_rank);
   const AdEntry* table = static_cast<const AdEntry*>(set->table);
   const double flops = 2.0 * seg.N * set->max_rank;
   {
     HostTimer tm(s, "adapter_shrink", flops * set->n, (double)seg.N * set->n * es);
     ShrinkArgs a{};
-    a.job[0] = ShrinkJob{X, nullptr, p.T, ldx, 0, (int)set->n};
+    a.job[0] = ShrinkJob{X, nullptr, p.F, ldx, (int)set->n, 0};
+    a.info = p.info;
     a.seg = seg;
     a.table = table;
-    a.rpmax = p.rpmax;
     const bool vec = al16(X) && ldx * es % 16 == 0 && set->n * es % 16 == 0 && (set->layout & LAY_A16);
-    launch_shrink<E>(a, p.tiles, 1, rt, vec, s);
+    launch_shrink<E>(a, p, 1, 0, vec, s);
   }
   {
     HostTimer tm(s, "adapter_expand", flops * set->m, 2.0 * seg.N * set->m * es);
     ExpandArgs a{};
-    a.Y = Y; a.ldy = ldy; a.width = (int)set->m; a.T = p.T; a.seg = seg; a.table = table; a.rpmax = p.rpmax;
-    launch_expand<E>(a, p.tiles, rt, (set->layout & LAY_B16) != 0, s);
+    a.Y = Y; a.ldy = ldy; a.width = (int)set->m;
+    launch_expand<E>(a, p, (set->layout & LAY_B16) != 0, s);
   }
   return host_check_launch("adapters forward");
 }
@@ -763,30 +1037,29 @@ template <typename E>
 int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, int64_t ldx, const void* dY,
                   int64_t lddy, void* dX, int64_t lddx, const AdPlan& p, hipStream_t s) {
   const size_t es = sizeof(E);
-  const int rt = rank_tiles(set->max_rank);
   const int m = (int)set->m, n = (int)set->n;
   const AdEntry* table = static_cast<const AdEntry*>(set->table);
   const double flops = 2.0 * seg.N * set->max_rank;
   const bool xvec = al16(X) && ldx * es % 16 == 0 && n * es % 16 == 0;
   const bool yvec = al16(dY) && lddy * es % 16 == 0 && m * es % 16 == 0;
-  {
-    HostTimer tm(s, "adapter_prep", 0.0, 2.0 * set->rows * (m + n) * es);
-    const int tw = set->max_rank > 96 ? 32 : 64;   // at most 33 KB of LDS
-    PrepArgs a{seg, table, p.list, p.offs, p.Bt, p.At, m, n, p.mp, (int)p.tiles, tw};
-    const unsigned grid = (unsigned)(set->count * (1 + (m + tw - 1) / tw + (n + tw - 1) / tw));
-    const size_t lds = (size_t)tw * (set->max_rank + 1) * sizeof(E);
-    hipLaunchKernelGGL(adapter_prep_kernel<E>, dim3(grid), dim3(256), lds < 64 ? 64 : lds, s, a);
-  }
-  if (p.tiles > 0) {
+  const ListArgs lists{p.list, p.offs, (int)p.tiles};
+  if (p.tiles == 0) {
+    hipLaunchKernelGGL(adapter_list_kernel, dim3((unsigned)set->count), dim3(512), 0, s, seg, lists);
+  } else {
     {
       HostTimer tm(s, "adapter_shrink", flops * (m + n), (double)seg.N * (m + n) * es);
       ShrinkArgs a{};
-      a.job[0] = ShrinkJob{X, nullptr, p.T, ldx, 0, n};
-      a.job[1] = ShrinkJob{dY, p.Bt, p.U, lddy, p.mp, m};
+      a.job[0] = ShrinkJob{X, p.T, nullptr, ldx, n, 0};
+      a.job[1] = ShrinkJob{dY, p.U, dX ? p.F : nullptr, lddy, m, 1};
       a.seg = seg;
       a.table = table;
-      a.rpmax = p.rpmax;
-      launch_shrink<E>(a, p.tiles, 2, rt, xvec && yvec && (set->layout & LAY_A16), s);
+      a.info = p.info;
+      a.lists = lists;
+      // columns of A turned by a workgroup: a power of two whose ranks fit the LDS
+      int tw = 64;
+      while (tw > 16 && (size_t)tw * (set->max_rank + 3) * es > TURN_LDS) tw /= 2;
+      a.turn = TurnArgs{dX ? p.At : nullptr, n, (n + tw - 1) / tw, tw};
+      launch_shrink<E>(a, p, 2, set->count * (1 + (dX ? a.turn.per : 0)), xvec && yvec && set->layout == (LAY_A16 | LAY_B16), s);
     }
     {
       HostTimer tm(s, "adapter_outer", 2 * flops * (m + n), (double)seg.N * (m + n) * es);
@@ -794,17 +1067,18 @@ int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, i
       a.job[0] = OuterJob{X, p.U, p.part[0], ldx, n};
       a.job[1] = OuterJob{dY, p.T, p.part[1], lddy, m};
       a.list = p.list; a.offs = p.offs; a.count = set->count; a.rpmax = p.rpmax; a.run = p.run; a.groups = p.groups;
+      a.N = seg.N;
       const int slab = 4 * 16 * El<E>::EL, wide = m > n ? m : n;
       const dim3 grid((unsigned)((wide + slab - 1) / slab), (unsigned)p.runs, (unsigned)(2 * p.groups));
-      if (rt == 1) outer<E, 1>(a, grid, xvec && yvec, s);
-      else if (rt == 2) outer<E, 2>(a, grid, xvec && yvec, s);
+      if (p.rpmax == 16) outer<E, 1>(a, grid, xvec && yvec, s);
+      else if (p.rpmax == 32) outer<E, 2>(a, grid, xvec && yvec, s);
       else outer<E, 4>(a, grid, xvec && yvec, s);
     }
     if (dX) {
       HostTimer tm(s, "adapter_expand", flops * n, 2.0 * seg.N * n * es);
       ExpandArgs a{};
-      a.Y = dX; a.ldy = lddx; a.width = n; a.W = p.At; a.T = p.U; a.seg = seg; a.table = table; a.rpmax = p.rpmax;
-      launch_expand<E>(a, p.tiles, rt, true, s);
+      a.Y = dX; a.ldy = lddx; a.width = n;
+      launch_expand<E>(a, p, true, s);
     }
   }
   {
@@ -813,9 +1087,8 @@ int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, i
     a.part[0] = p.part[0]; a.part[1] = p.part[1];
     a.offs = p.offs; a.table = table; a.width[0] = n; a.width[1] = m; a.rpmax = p.rpmax; a.run = p.run;
     a.accumulate = (set->flags & POETX_ACCUMULATE_GRAD) != 0;
-    const int64_t most = (int64_t)set->max_rank * (m > n ? m : n);
-    hipLaunchKernelGGL(adapter_reduce_kernel, dim3((unsigned)((most + 255) / 256), (unsigned)set->count, 2), dim3(256),
-                       0, s, a);
+    hipLaunchKernelGGL(adapter_reduce_kernel, dim3((unsigned)(((m > n ? m : n) + 63) / 64), (unsigned)set->count,
+                                                   (unsigned)(2 * ((set->max_rank + 15) / 16))), dim3(256), 0, s, a);
   }
   return host_check_launch("adapters backward");
 }
