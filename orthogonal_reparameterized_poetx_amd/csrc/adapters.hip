@@ -13,7 +13,7 @@
 // so that a tile finds its segment by a search and no launch has to lay the
 // tiles out first.
 #include "../../include/poetx.h"
-#include "common.h"
+#include "global.h"
 #include "host.h"
 
 namespace poetx {
@@ -55,11 +55,9 @@ __device__ __forceinline__ AdTile find_tile(const AdSegs& g, int w) {
   int lo = 0, len = g.nseg;
   for (;;) {
     const int step = (len + 63) >> 6;
-    const int s = lo + lane * step;
     const bool in = lane * step < len;
-    const int a = in ? clamp_token(g.start[s], g.N) : 0;
-    const int b = in && step == 1 ? clamp_token(g.start[s + 1], g.N) : 0;
-    const int ad = in && step == 1 ? g.which[s] : -1;
+    const int s = lo + (in ? lane * step : 0);
+    const int a = clamp_token(g.start[s], g.N), b = clamp_token(g.start[s + 1], g.N), ad = g.which[s];
     const int k = __popcll(__ballot(in && a / AD_T + s <= w));
     if (k == 0) return AdTile{0, 0, 0};
     if (step == 1) {
@@ -110,12 +108,12 @@ template <> struct El<float> {
 template <typename E, bool VEC>
 __device__ __forceinline__ uint4 load_frag(const E* row, int k, int width, const E* end) {
   constexpr int EL = El<E>::EL;
-  if (VEC) return k < width ? ldg16(row + k) : make_uint4(0, 0, 0, 0);
+  if (VEC) return k < width ? gld16(row + k) : make_uint4(0, 0, 0, 0);
   const int left = width - k;
   uint4 v = make_uint4(0, 0, 0, 0);
   if (left <= 0) return v;
   if (row + k + EL <= end) {
-    __builtin_memcpy(&v, row + k, 16);
+    v = gld16_u(row + k);
     if (left < EL) {
       uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -129,7 +127,7 @@ __device__ __forceinline__ uint4 load_frag(const E* row, int k, int width, const
   }
   E e[EL];
 #pragma unroll
-  for (int i = 0; i < EL; ++i) e[i] = i < left ? row[k + i] : E(0);
+  for (int i = 0; i < EL; ++i) e[i] = i < left ? gld(row + k + i) : E(0);
   return __builtin_bit_cast(uint4, e);
 }
 
@@ -237,7 +235,7 @@ __device__ __forceinline__ void turn_a(const AdEntry* table, const TurnArgs& p, 
   const int ld = ad.r + (sizeof(E) == 2 ? 2 + (ad.r & 1) : 1);
   if (lane < cols)
 #pragma unroll 4
-    for (int r = row; r < ad.r; r += rows) lds[lane * ld + r] = A[(int64_t)r * p.n + lane];
+    for (int r = row; r < ad.r; r += rows) lds[lane * ld + r] = gld(A + (int64_t)r * p.n + lane);
   __syncthreads();
   E* out = static_cast<E*>(p.At) + (int64_t)ad.row0 * p.n + (int64_t)c0 * ad.rp;
   const int total = cols * ad.rp;
@@ -300,7 +298,7 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int k = k0 + h * KF + g * EL;   // fragment h of a step: element k0 + h KF + g EL + e
-          if (FULL && VEC) xf[u][s][h] = ldg16(x[s] + k);
+          if (FULL && VEC) xf[u][s][h] = gld16(x[s] + k);
           else xf[u][s][h] = load_frag<E, VEC>(x[s], k, J.width, xend);
         }
       if constexpr (STAGE) {
@@ -327,10 +325,10 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
               if constexpr (USEB) {
                 E e[EL];
 #pragma unroll
-                for (int q = 0; q < EL; ++q) e[q] = k + q < J.width ? W[(int64_t)(k + q) * ad.r + rr] : E(0);
+                for (int q = 0; q < EL; ++q) e[q] = k + q < J.width ? gld(W + (int64_t)(k + q) * ad.r + rr) : E(0);
                 wf[u][i][h] = __builtin_bit_cast(uint4, e);
               } else if (FULL && VEC) {
-                wf[u][i][h] = ldg16(W + (int64_t)rr * J.width + k);
+                wf[u][i][h] = gld16(W + (int64_t)rr * J.width + k);
               } else {
                 wf[u][i][h] = load_frag<E, VEC>(W + (int64_t)rr * J.width, k, J.width, wend);
               }
@@ -544,7 +542,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a)
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int h = 0; h < NH; ++h)
-        if (h * 4 * EL < left && 16 * s + l16 < in.rows) yv[s][h] = ldg16(y[s] + h * 4 * EL);
+        if (h * 4 * EL < left && 16 * s + l16 < in.rows) yv[s][h] = gld16(y[s] + h * 4 * EL);
   }
   f32x4 acc[4][2];
 #pragma unroll
@@ -618,12 +616,9 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a)
 #pragma unroll
       for (int e = 0; e < EL; ++e) v[e] = acc[h * CP + (e >> 2)][s][e & 3];
       if (VECY) {
-        if (n > 0) stg16(o, add_frag<E>(yv[s][h], v));
+        if (n > 0) gst16(o, add_frag<E>(yv[s][h], v));
       } else if (n >= EL) {
-        uint4 x;
-        __builtin_memcpy(&x, o, 16);
-        x = add_frag<E>(x, v);
-        __builtin_memcpy(o, &x, 16);
+        gst16_u(o, add_frag<E>(gld16_u(o), v));
       } else {
 #pragma unroll
         for (int e = 0; e < EL; ++e)
@@ -816,7 +811,7 @@ __global__ __launch_bounds__(256) void adapter_reduce_kernel(const ReduceArgs a)
     for (int i = 0; i < 4; ++i)
       if (rank + i < e.r && col < width) {
         float* dst = out + (int64_t)(rank + i) * width + col;
-        *dst = a.accumulate ? *dst + v[i] : v[i];
+        gst(dst, a.accumulate ? gld(dst) + v[i] : v[i]);
       }
     return;
   }
@@ -830,7 +825,7 @@ __global__ __launch_bounds__(256) void adapter_reduce_kernel(const ReduceArgs a)
     const int j = blockIdx.x * 64 + c;
     if (rr < ranks && j < width) {
       float* dst = out + (int64_t)j * e.r + rank0 + rr;
-      *dst = a.accumulate ? *dst + turn[c][rr] : turn[c][rr];
+      gst(dst, a.accumulate ? gld(dst) + turn[c][rr] : turn[c][rr]);
     }
   }
 }

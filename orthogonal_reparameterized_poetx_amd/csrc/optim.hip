@@ -11,7 +11,7 @@
 #include <cstring>
 
 #include "../../include/poetx.h"
-#include "common.h"
+#include "global.h"
 #include "host.h"
 
 namespace poetx {
@@ -114,30 +114,30 @@ __device__ __forceinline__ F4 load4(const void* base, int64_t at, int left, bool
   F4 r;
   if (vec && left >= 4) {
     if (bf) {
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+      const u32x2 w = *(const POETX_GLOBAL u32x2*)(static_cast<const uint16_t*>(base) + at);
       r.x[0] = __uint_as_float(w.x << 16); r.x[1] = __uint_as_float(w.x & 0xffff0000u);
       r.x[2] = __uint_as_float(w.y << 16); r.x[3] = __uint_as_float(w.y & 0xffff0000u);
     } else {
-      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-      r.x[0] = w.x; r.x[1] = w.y; r.x[2] = w.z; r.x[3] = w.w;
+      const f32x4 w = *(const POETX_GLOBAL f32x4*)(static_cast<const float*>(base) + at);
+      r.x[0] = w[0]; r.x[1] = w[1]; r.x[2] = w[2]; r.x[3] = w[3];
     }
     return r;
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    r.x[j] = j >= left ? 0.f : bf ? bits_to_f32(static_cast<const uint16_t*>(base)[at + j])
-                                  : static_cast<const float*>(base)[at + j];
+    r.x[j] = j >= left ? 0.f : bf ? bits_to_f32(gld(static_cast<const uint16_t*>(base) + at + j))
+                                  : gld(static_cast<const float*>(base) + at + j);
   return r;
 }
 
 __device__ __forceinline__ void store4_bf16(uint16_t* base, int64_t at, int left, bool vec, const uint16_t h[4]) {
   if (vec && left >= 4) {
-    *reinterpret_cast<uint2*>(base + at) = make_uint2(pack2(h[0], h[1]), pack2(h[2], h[3]));
+    *(POETX_GLOBAL u32x2*)(base + at) = u32x2{pack2(h[0], h[1]), pack2(h[2], h[3])};
     return;
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (j < left) base[at + j] = h[j];
+    if (j < left) gst(base + at + j, h[j]);
 }
 
 struct StepArgs {
@@ -225,11 +225,11 @@ __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
     } else {
       float* dst = static_cast<float*>(t.p) + at;
       if (t.vec && left[i] == 4) {
-        *reinterpret_cast<float4*>(dst) = make_float4(p[i].x[0], p[i].x[1], p[i].x[2], p[i].x[3]);
+        *(POETX_GLOBAL f32x4*)dst = f32x4{p[i].x[0], p[i].x[1], p[i].x[2], p[i].x[3]};
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (j < left[i]) dst[j] = p[i].x[j];
+          if (j < left[i]) gst(dst + j, p[i].x[j]);
       }
       if (t.copy) store4_bf16(t.copy, at, left[i], t.vec, cb);
     }
