@@ -79,8 +79,6 @@ struct AdInfo {
   int32_t ldw, pad[3];
 };
 
-template <int V> struct Int { static constexpr int value = V; };
-
 // ---- element types.  A fragment is 16 bytes of a row: EL elements; the four
 // lane groups of a wave hold KF = 4 EL elements of the contraction.  bf16: one
 // 16x16x32 MFMA; fp32: four 16x16x4 MFMAs, element e of every group in MFMA e.
@@ -131,21 +129,22 @@ __device__ __forceinline__ uint4 load_frag(const E* row, int k, int width, const
   return __builtin_bit_cast(uint4, e);
 }
 
-// ---- shrink: T of each tile, fp32, in one or both of two orders:
-//   rows   [rank][32 tokens], for the gradients
-//   frags  as the expand's lanes hold it: [step kk][half s][lane][EL], the value of
-//          rank kk KF + EL (lane / 16) + e and token 16 s + lane % 16 (bf16 sets of
-//          rank 16: [half][lane < 32][8])
-// A workgroup takes a tile, RT rank tiles and a part of the width; its eight
-// waves take every eighth step of 64 (fp32: 32) elements of that part, and add
-// their sums in LDS.  Each wave issues the loads of several steps before the
-// first product, so that one latency covers them.
+// ---- shrink: T of each tile, fp32, as the expand's lanes hold it ("frags"):
+// [step kk][half s][lane][EL], the value of rank kk KF + EL (lane / 16) + e and
+// token 16 s + lane % 16 (bf16 sets of rank 16: [half][lane < 32][8]).
+// A workgroup takes a tile, RT rank tiles and a part of the width, which goes
+// through LDS in chunks: rows of a KiB (or half) are read whole, and each wave
+// multiplies a quarter of the chunk's columns; at the end the waves' sums are
+// added.  Who reads T adds the parts.  Reading the operands of the products
+// straight from memory, 16 rows of 64 bytes an instruction, took 1.4 to 1.7 times
+// as long (rows a power of two apart lie in the same channel of the caches, and
+// all workgroups ask for the same columns at once): 8192 rows of 11008 47.8 us
+// against 33.3 us, the rows read in order (without products).
 struct ShrinkJob {
   const void* X;      // [N][width], rows ldx apart
-  float* rows;        // [tiles][rpmax * 32], nullable
-  float* frags;       // [parts][tiles][rpmax * 32], nullable
+  float* T;           // [parts][tiles][rpmax * 32]
   int64_t ldx;
-  int width;
+  int width, parts;
   int useB;           // weights: each adapter's A [rank][width] or B [width][rank]
 };
 struct ListArgs {     // see build_list
@@ -164,8 +163,8 @@ struct ShrinkArgs {
   AdInfo* info;       // of each tile, for the expand
   ListArgs lists;     // extra workgroups after the tiles': count lists, then count * turn.per transposes
   TurnArgs turn;
-  int rpmax, tiles, parts, groups;   // groups: rank groups of RT tiles; grid.y = jobs * groups * parts
-};
+  int rpmax, tiles, pw, groups;   // pw: columns of a part; groups: rank groups of RT tiles
+};                                // grid.x: rank groups of the parts of the jobs; grid.y, z: tiles, then the extra work
 
 // the tiles of each adapter, one adapter after another, for the gradients:
 // entry {t0, rows, adapter, tile index}; offs[a] the first entry of adapter a
@@ -249,183 +248,170 @@ __device__ __forceinline__ void turn_a(const AdEntry* table, const TurnArgs& p, 
   }
 }
 
-constexpr int SHRINK_WAVES = 8;
-constexpr int TURN_LDS = 32 * 1024;   // bytes a transpose may take
-// LDS bytes of B's rows of one step for all waves (bf16), of the sums and of a transpose
-constexpr int shrink_lds(int rt, bool bf) {
-  const int stage = bf ? SHRINK_WAVES * 64 * 16 * rt * 2 : 0, red = SHRINK_WAVES * 512 * 4;
-  const int most = stage > red ? stage : red;
+constexpr int SHRINK_WAVES = 4;
+constexpr int TURN_LDS = 16 * 1024;   // bytes a transpose may take
+// a chunk: bytes of a row; LDS bytes of a row of x or A, of x, of the weights
+constexpr int shrink_rb(int rt) { return rt == 1 ? 1024 : 512; }
+constexpr int shrink_row(int rt) { return shrink_rb(rt) + 16; }
+constexpr int shrink_x(int rt) { return AD_T * shrink_row(rt); }
+constexpr int shrink_w(int rt, int es) {
+  const int byA = 16 * rt * shrink_row(rt), byB = shrink_rb(rt) / es * (16 * rt + (es == 4 ? 4 : 0)) * es;
+  return byA > byB ? byA : byB;
+}
+constexpr int shrink_lds(int rt, int es) {
+  const int most = shrink_x(rt) + shrink_w(rt, es);
   return most > TURN_LDS ? most : TURN_LDS;
 }
 
 template <typename E, int RT, bool VEC, bool USEB>
 __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob& J, const AdTile& tile, int w,
                                             int group, int part, char* lds) {
-  constexpr int EL = El<E>::EL, KF = El<E>::KF, STEP = 2 * KF;
-  constexpr bool STAGE = USEB && EL == 8;   // B's rows through LDS, read transposed
+  constexpr int EL = El<E>::EL, KF = El<E>::KF, ES = sizeof(E), THREADS = 64 * SHRINK_WAVES;
+  constexpr int RB = shrink_rb(RT), CW = RB / ES, LD = shrink_row(RT) / ES, PR = RB / 16;   // PR: pieces of a row
+  constexpr int NX = AD_T * PR / THREADS, NW = 16 * RT * PR / THREADS;                    // pieces of a thread
+  constexpr int NF = CW / SHRINK_WAVES / KF;                                              // fragments of a wave
   const AdEntry ad = a.table[tile.adapter];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int rank0 = group * RT * 16;
   if (rank0 >= ad.rp) return;
   const int rt_n = (ad.rp - rank0) >> 4;   // rank tiles of this adapter from rank0 on
-  const E* x[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int t = 16 * s + l16;
-    x[s] = static_cast<const E*>(J.X) + (int64_t)(tile.t0 + (t < tile.rows ? t : 0)) * J.ldx;
-  }
+  const E* X = static_cast<const E*>(J.X) + (int64_t)tile.t0 * J.ldx;
   const E* xend = static_cast<const E*>(J.X) + (int64_t)(a.seg.N - 1) * J.ldx + J.width;
   const E* W = static_cast<const E*>(USEB ? ad.B : ad.A);
   const E* wend = W + (int64_t)ad.r * J.width;
-  uint16_t* stage = reinterpret_cast<uint16_t*>(lds) + wave * 64 * 16 * RT;
-  // staged rows hold the ranks rank0 .. rank0 + rw of B in rc pieces of eight
-  const int rw = ad.r - rank0 < 16 * RT ? ad.r - rank0 : 16 * RT, rc = (rw + 7) >> 3, ldst = rc * 8;
+  E* lx = reinterpret_cast<E*>(lds);
+  E* lw = reinterpret_cast<E*>(lds + shrink_x(RT));
+  // B: rows of the chunk, the ranks rank0 .. rank0 + rw in rc pieces, ldb elements apart
+  const int rw = ad.r - rank0 < 16 * RT ? ad.r - rank0 : 16 * RT, rc = (rw + EL - 1) / EL;
+  const int ldb = rc * EL + (ES == 4 ? 4 : 0);
+  int brow[USEB ? NW : 1], bcol[USEB ? NW : 1];
+  if constexpr (USEB) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int c = i * THREADS + tid;
+      brow[i] = c / rc;
+      bcol[i] = (c - brow[i] * rc) * EL;
+    }
+  }
   f32x4 acc[RT][2];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // UU steps from st on, every eighth; FULL: within the width
-  auto run = [&](auto uu, auto full, int st) {
-    constexpr int UU = decltype(uu)::value;
-    constexpr bool FULL = decltype(full)::value;
-    uint4 xf[UU][2][2], wf[UU][RT][2];
+  uint4 xr[NX], wr[NW];
+  auto load = [&](int k0) {   // the chunk from column k0 on
 #pragma unroll
-    for (int u = 0; u < UU; ++u) {
-      const int k0 = (st + u * SHRINK_WAVES) * STEP;
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k = k0 + h * KF + g * EL;   // fragment h of a step: element k0 + h KF + g EL + e
-          if (FULL && VEC) xf[u][s][h] = gld16(x[s] + k);
-          else xf[u][s][h] = load_frag<E, VEC>(x[s], k, J.width, xend);
-        }
-      if constexpr (STAGE) {
-        // piece c of the step: row c / rc, ranks 8 (c % rc) on; 64 rows hold 64 rc pieces
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = (2 * i + h) * 64 + lane;
-            const int row = rc == 2 ? c >> 1 : rc == 4 ? c >> 2 : rc == 8 ? c >> 3 : c / rc;
-            const int j = k0 + row, cc = c - row * rc;
-            wf[u][i][h] = row < 64 && (FULL || j < J.width)
-                              ? load_frag<E, VEC>(W + (int64_t)j * ad.r + rank0, cc * 8, rw, wend)
-                              : make_uint4(0, 0, 0, 0);
-          }
-      } else {
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const int rank = rank0 + 16 * i + l16, rr = rank < ad.r ? rank : 0;
-          if (i < rt_n) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int k = k0 + h * KF + g * EL;
-              if constexpr (USEB) {
-                E e[EL];
-#pragma unroll
-                for (int q = 0; q < EL; ++q) e[q] = k + q < J.width ? gld(W + (int64_t)(k + q) * ad.r + rr) : E(0);
-                wf[u][i][h] = __builtin_bit_cast(uint4, e);
-              } else if (FULL && VEC) {
-                wf[u][i][h] = gld16(W + (int64_t)rr * J.width + k);
-              } else {
-                wf[u][i][h] = load_frag<E, VEC>(W + (int64_t)rr * J.width, k, J.width, wend);
-              }
-            }
-          }
-        }
-      }
+    for (int i = 0; i < NX; ++i) {
+      const int c = i * THREADS + tid, row = c / PR, k = k0 + c % PR * EL;
+      xr[i] = load_frag<E, VEC>(X + (int64_t)(row < tile.rows ? row : 0) * J.ldx, k, J.width, xend);
     }
 #pragma unroll
-    for (int u = 0; u < UU; ++u) {
-      if constexpr (STAGE) {
-        // LDS operations of a wave stay in order: the rows are in place before
-        // they are read, and read before the next step's are written
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = (2 * i + h) * 64 + lane;
-            if (c < 64 * rc) *reinterpret_cast<uint4*>(stage + c * 8) = wf[u][i][h];
-          }
-        asm volatile("" ::: "memory");
+    for (int i = 0; i < NW; ++i) {
+      if constexpr (USEB) {
+        const int j = k0 + brow[i];
+        wr[i] = brow[i] < CW && j < J.width ? load_frag<E, VEC>(W + (int64_t)j * ad.r + rank0, bcol[i], rw, wend)
+                                            : make_uint4(0, 0, 0, 0);
+      } else {
+        const int c = i * THREADS + tid, rank = rank0 + c / PR, k = k0 + c % PR * EL;
+        wr[i] = load_frag<E, VEC>(W + (int64_t)(rank < ad.r ? rank : 0) * J.width, k, J.width, wend);
       }
+    }
+  };
+  const int k_end = (part + 1) * a.pw < J.width ? (part + 1) * a.pw : J.width;
+  int k0 = part * a.pw;
+  load(k0);
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int c = i * THREADS + tid;
+      *reinterpret_cast<uint4*>(lx + c / PR * LD + c % PR * EL) = xr[i];
+    }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int c = i * THREADS + tid;
+      if constexpr (USEB) {
+        if (brow[i] < CW) *reinterpret_cast<uint4*>(lw + brow[i] * ldb + bcol[i]) = wr[i];
+      } else {
+        *reinterpret_cast<uint4*>(lw + c / PR * LD + c % PR * EL) = wr[i];
+      }
+    }
+    __syncthreads();
+    k0 += CW;
+    const bool more = k0 < k_end;
+    if (more) load(k0);   // on its way while this chunk is multiplied
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const int kf = (wave * NF + f) * KF;   // of the chunk
+      uint4 xf[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) xf[s] = *reinterpret_cast<const uint4*>(lx + (16 * s + l16) * LD + kf + g * EL);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         if (i < rt_n) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint4 f = wf[u][i][h];
-            if constexpr (STAGE) {
-              // 16 lanes read 4 rows of 16 ranks and get 4 rows of their own rank
-              // (past the staged pieces: another's, whose sums are dropped)
-              const int col = 16 * i + 4 * (l16 & 3) < ldst ? 16 * i + 4 * (l16 & 3) : 0;
-              const uint16_t* src = stage + (h * 32 + 8 * g + (l16 >> 2)) * ldst + col;
-              const i16x4 p = ds_read_tr16a(src), q = ds_read_tr16a(src + 4 * ldst);
-              typedef short i16x8 __attribute__((ext_vector_type(8)));
-              f = __builtin_bit_cast(uint4, i16x8{p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]});
-            }
-            acc[i][0] = El<E>::mma(f, xf[u][0][h], acc[i][0]);
-            acc[i][1] = El<E>::mma(f, xf[u][1][h], acc[i][1]);
+          uint4 wf;
+          if constexpr (!USEB) {
+            wf = *reinterpret_cast<const uint4*>(lw + (16 * i + l16) * LD + kf + g * EL);
+          } else if constexpr (ES == 2) {
+            // 16 lanes read 4 rows of 16 ranks and get 4 rows of their own rank
+            // (past the pieces: another's, whose sums are dropped)
+            const int col = 16 * i + 4 * (l16 & 3) < ldb ? 16 * i + 4 * (l16 & 3) : 0;
+            const uint16_t* src = lw + (kf + 8 * g + (l16 >> 2)) * ldb + col;
+            const i16x4 p = ds_read_tr16a(src), q = ds_read_tr16a(src + 4 * ldb);
+            typedef short i16x8 __attribute__((ext_vector_type(8)));
+            wf = __builtin_bit_cast(uint4, i16x8{p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]});
+          } else {
+            const int col = 16 * i + l16 < ldb ? 16 * i + l16 : 0;
+            const E* src = lw + (kf + 4 * g) * ldb + col;
+            wf = make_uint4(__builtin_bit_cast(uint32_t, src[0]), __builtin_bit_cast(uint32_t, src[ldb]),
+                            __builtin_bit_cast(uint32_t, src[2 * ldb]), __builtin_bit_cast(uint32_t, src[3 * ldb]));
           }
+          acc[i][0] = El<E>::mma(wf, xf[0], acc[i][0]);
+          acc[i][1] = El<E>::mma(wf, xf[1], acc[i][1]);
         }
       }
-      if constexpr (STAGE) asm volatile("" ::: "memory");
     }
-  };
-  // the part's whole steps, then (last part) the rest of the width
-  const int steps = J.width / STEP, per = (steps + a.parts - 1) / a.parts;
-  const int s_end = (part + 1) * per < steps ? (part + 1) * per : steps;
-  constexpr int U = RT == 1 ? 4 : 2;
-  int st = part * per + wave;
-  for (; st + (U - 1) * SHRINK_WAVES < s_end; st += U * SHRINK_WAVES) run(Int<U>{}, Int<1>{}, st);
-  if (U > 2 && st + SHRINK_WAVES < s_end) {
-    run(Int<2>{}, Int<1>{}, st);
-    st += 2 * SHRINK_WAVES;
+    __syncthreads();
+    if (!more) break;
   }
-  if (st < s_end) run(Int<1>{}, Int<1>{}, st);
-  if (steps * STEP < J.width && part == a.parts - 1 && wave == SHRINK_WAVES - 1) run(Int<1>{}, Int<0>{}, steps);
-
   float* red = reinterpret_cast<float*>(lds);
-  const int64_t size = (int64_t)a.rpmax * AD_T;
-  float* rows = J.rows ? J.rows + w * size : nullptr;
-  float* frags = J.frags ? J.frags + ((int64_t)part * a.tiles + w) * size : nullptr;
-  if (STAGE) __syncthreads();
+  float* T = J.T + ((int64_t)part * a.tiles + w) * a.rpmax * AD_T;
+  const int lanes = a.rpmax < KF ? 16 * (a.rpmax / EL) : 64;
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     if (i < rt_n) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) *reinterpret_cast<f32x4*>(&red[wave * 512 + s * 256 + lane * 4]) = acc[i][s];
       __syncthreads();
-      float v = 0.f;
 #pragma unroll
-      for (int q = 0; q < SHRINK_WAVES; ++q) v += red[q * 512 + tid];
-      const int rank = rank0 + 16 * i + 4 * ((tid >> 6) & 3) + (tid & 3), s = tid >> 8, c = (tid >> 2) & 15;
-      const int t = 16 * s + c;
-      v = rank < ad.r && t < tile.rows ? v * ad.scale : 0.f;
-      if (rows) rows[rank * AD_T + t] = v;
-      if (frags) {
-        const int kk = rank / KF, gg = rank % KF / EL, e = rank % EL, lanes = a.rpmax < KF ? 16 * (a.rpmax / EL) : 64;
-        frags[((kk * 2 + s) * lanes + gg * 16 + c) * EL + e] = v;
+      for (int s = 0; s < 2; ++s) {
+        float v = 0.f;
+#pragma unroll
+        for (int q = 0; q < SHRINK_WAVES; ++q) v += red[q * 512 + s * 256 + tid];
+        const int rank = rank0 + 16 * i + 4 * (tid >> 6) + (tid & 3), c = (tid >> 2) & 15;
+        v = rank < ad.r && 16 * s + c < tile.rows ? v * ad.scale : 0.f;
+        const int kk = rank / KF, gg = rank % KF / EL, e = rank % EL;
+        T[((kk * 2 + s) * lanes + gg * 16 + c) * EL + e] = v;
       }
       __syncthreads();
     }
   }
 }
 
+constexpr int TILES_Y = 32768;   // tiles along the grid's second dimension
+
 template <typename E, int RT, bool VEC>
-__global__ __launch_bounds__(512) void adapter_shrink_kernel(const ShrinkArgs a) {
-  __shared__ __align__(16) char lds[shrink_lds(RT, sizeof(E) == 2)];
-  const int w = blockIdx.x;
+__global__ __launch_bounds__(64 * SHRINK_WAVES) void adapter_shrink_kernel(const ShrinkArgs a) {
+  __shared__ __align__(16) char lds[shrink_lds(RT, sizeof(E))];
+  const int64_t w = (int64_t)blockIdx.z * TILES_Y + blockIdx.y;
   if (w >= a.tiles) {
-    if (blockIdx.y) return;
-    if (w - a.tiles < a.seg.count) build_list<512>(a.seg, a.lists, w - a.tiles, reinterpret_cast<int*>(lds));
-    else turn_a<E>(a.table, a.turn, w - a.tiles - a.seg.count, lds);
+    const int64_t x = w - a.tiles;
+    if (blockIdx.x || !a.lists.list) return;
+    if (x < a.seg.count) build_list<64 * SHRINK_WAVES>(a.seg, a.lists, (int)x, reinterpret_cast<int*>(lds));
+    else if (a.turn.At && x - a.seg.count < (int64_t)a.seg.count * a.turn.per)
+      turn_a<E>(a.table, a.turn, (int)(x - a.seg.count), lds);
     return;
   }
-  const AdTile tile = find_tile(a.seg, w);
-  if (blockIdx.y == 0 && threadIdx.x == 0) {
+  const AdTile tile = find_tile(a.seg, (int)w);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
     AdInfo in{tile.t0, tile.rows, nullptr, 0, {0, 0, 0}};
     if (tile.rows) {
       const AdEntry ad = a.table[tile.adapter];
@@ -435,10 +421,13 @@ __global__ __launch_bounds__(512) void adapter_shrink_kernel(const ShrinkArgs a)
     a.info[w] = in;
   }
   if (tile.rows == 0) return;
-  const int part = blockIdx.y % a.parts, group = blockIdx.y / a.parts % a.groups;
-  const ShrinkJob& J = a.job[blockIdx.y / (a.parts * a.groups)];
-  if (J.useB) shrink_body<E, RT, VEC, true>(a, J, tile, w, group, part, lds);
-  else shrink_body<E, RT, VEC, false>(a, J, tile, w, group, part, lds);
+  int x = blockIdx.x;
+  const int n0 = a.job[0].parts * a.groups;
+  const ShrinkJob& J = a.job[x >= n0];
+  if (x >= n0) x -= n0;
+  const int part = x / a.groups, group = x % a.groups;
+  if (J.useB) shrink_body<E, RT, VEC, true>(a, J, tile, (int)w, group, part, lds);
+  else shrink_body<E, RT, VEC, false>(a, J, tile, (int)w, group, part, lds);
 }
 
 // ---- expand: Y[t][j] += sum_k T[k][t] W[j][k], W = each adapter's B, or (dx) At
@@ -448,7 +437,11 @@ struct ExpandArgs {
   int width;
   const float* T;       // frags [parts][tiles][rpmax * 32], the parts to be added
   const AdInfo* info;
-  int rpmax, tiles, parts;
+  int rpmax, tiles, parts, cols;   // cols: column groups; the grid's x past them: sums
+  // (backward) sums of the parts in the order [rank][32 tokens], for the gradients
+  const float* F[2];
+  float* rows[2];
+  int fparts[2];
 };
 
 // 8 (bf16) fp32 values as bf16 pairs: hi, and lo = value - hi, which keep 16 bits of the value
@@ -482,6 +475,19 @@ __device__ __forceinline__ void transpose8(const uint4 x[8], uint4 op[8]) {
   }
 }
 
+// exchanges a's lanes 32..63 with b's lanes 0..31
+__device__ __forceinline__ void swap32(uint4& a, uint4& b) {
+  uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x[q], y[q], false, false);
+    x[q] = r[0];
+    y[q] = r[1];
+  }
+  a = make_uint4(x[0], x[1], x[2], x[3]);
+  b = make_uint4(y[0], y[1], y[2], y[3]);
+}
+
 // y + v for EL elements
 template <typename E>
 __device__ __forceinline__ uint4 add_frag(uint4 y, const float* v) {
@@ -498,15 +504,33 @@ __device__ __forceinline__ uint4 add_frag(uint4 y, const float* v) {
   return make_uint4(n[0], n[1], n[2], n[3]);
 }
 
-// A workgroup takes one tile and 256 columns, 64 a wave; column groups of a tile
+// A workgroup takes one tile and four waves' columns; column groups of a tile
 // follow one another in the grid.  Small workgroups in the order of the memory
-// are what in-place updates of Y want: the same kernel with runs of four tiles
-// a workgroup, W kept in registers and the next tile's Y fetched ahead
-// took 48 us where this order takes 3X us (8192 x 5632, rank 16).
+// are what in-place updates of Y want: runs of four tiles a workgroup, with W kept
+// in registers and the next tile's Y fetched ahead, took 48.6 us where one
+// tile a workgroup takes 40.6 us (8192 x 5632, rank 16; 128 columns a wave, whose
+// T is a quarter of the Y it moves; with 64 columns 43.0 us, with 32 46.9 us).
 // The MFMA's rows are the wave's columns, in an order that gives each lane EL
 // neighbouring columns of a token, and the four lanes of a token neighbouring
 // 16-byte pieces.
-constexpr int EXPAND_Y = 32768;   // tiles along the grid's second dimension
+// MFMAs across a wave's columns, 16 columns each:
+constexpr int expand_nc(int rt) { return rt == 1 ? 8 : 4; }
+
+template <typename E>
+__device__ __forceinline__ void sum_rows(const ExpandArgs& a, int64_t w, int job) {
+  constexpr int EL = El<E>::EL, KF = El<E>::KF;
+  const int64_t size = (int64_t)a.rpmax * AD_T;
+  const int lanes = a.rpmax < KF ? 16 * (a.rpmax / EL) : 64;
+  const float* F = a.F[job] + w * size;
+  float* rows = a.rows[job] + w * size;
+  for (int i = threadIdx.x; i < (int)size; i += 256) {
+    float v = F[i];
+#pragma unroll 4
+    for (int p = 1; p < a.fparts[job]; ++p) v += F[p * a.tiles * size + i];
+    const int e = i % EL, lane = i / EL % lanes, s = i / EL / lanes & 1, kk = i / EL / lanes >> 1;
+    rows[(kk * KF + (lane >> 4) * EL + e) * AD_T + 16 * s + (lane & 15)] = v;
+  }
+}
 
 template <typename E, int RT, bool VECY, bool VECW>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a) {
@@ -515,21 +539,48 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a)
   constexpr bool PACK = BF && RT == 1;   // 16 ranks: hi and lo side by side in one MFMA
   constexpr int NK = PACK ? 1 : RT * 16 / KF;
   constexpr int NP = BF && !PACK ? 2 : 1;
-  constexpr int NH = 16 / EL;            // 16-byte pieces of a lane and token
-  constexpr int CP = EL / 4;             // MFMAs of a piece
+  constexpr int NC = expand_nc(RT), CP = EL / 4;   // MFMAs of a wave, of a 16-byte piece
+  constexpr int NH = NC / CP;                      // 16-byte pieces of a lane and token
   constexpr int KU = RT <= 4 ? NK : 1;   // contraction steps whose operands are in flight together
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ __align__(16) float tl[RT * 512];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int jb = blockIdx.x * 256 + wave * 64;
-  const int64_t w = (int64_t)blockIdx.z * EXPAND_Y + blockIdx.y;
-  if (jb >= a.width || w >= a.tiles) return;
+  const int64_t w = (int64_t)blockIdx.z * TILES_Y + blockIdx.y;
+  if (w >= a.tiles) return;
   const AdInfo in = a.info[w];
+  if (in.rows == 0) return;
+  if ((int)blockIdx.x >= a.cols) {
+    sum_rows<E>(a, w, blockIdx.x - a.cols);
+    return;
+  }
+  const int jb = (blockIdx.x * 4 + wave) * 16 * NC;
+  // T, its parts added: two floats a thread and rank tile
+  const int64_t size = (int64_t)a.rpmax * AD_T;
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  f32x2 t[RT];
+  {
+    const float* T = a.T + w * size + tid * 2;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      t[i] = 16 * i < a.rpmax ? *reinterpret_cast<const f32x2*>(T + i * 512) : f32x2{0.f, 0.f};
+    // four parts' loads at a time
+    for (int p = 1; p < a.parts; p += 4) {
+      f32x2 q[4][RT];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          if (p + k < a.parts && 16 * i < a.rpmax)
+            q[k][i] = *reinterpret_cast<const f32x2*>(T + (p + k) * a.tiles * size + i * 512);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          if (p + k < a.parts) t[i] += q[k][i];
+    }
+  }
   // element e of contraction step kk: rank kk KF + kc + e
   const int kc = PACK ? 8 * (g & 1) : g * EL;
-  const int64_t size = (int64_t)a.rpmax * AD_T;
-  const float* T = a.T + w * size + (PACK ? (lane & 31) : lane) * EL;
-  constexpr int TS = PACK ? 32 * EL : 64 * EL;   // floats of one half of a step
-  if (in.rows == 0) return;
   const E* W = static_cast<const E*>(in.W);
   const E* wend = W + (int64_t)a.width * in.ldw;
   E* y[2];
@@ -544,61 +595,60 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a)
       for (int h = 0; h < NH; ++h)
         if (h * 4 * EL < left && 16 * s + l16 < in.rows) yv[s][h] = gld16(y[s] + h * 4 * EL);
   }
-  f32x4 acc[4][2];
+  uint4 wf[KU][NC];
+  auto load_w = [&](int k0) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) acc[c][0] = acc[c][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-  for (int k0 = 0; k0 < NK; k0 += KU) {
-    if (k0 > 0 && k0 * KF >= in.ldw) break;
-    uint4 wf[KU][4];
-    f32x4 t[KU][2][CP];
+    for (int u = 0; u < KU; ++u)
 #pragma unroll
-    for (int u = 0; u < KU; ++u) {
-      const int kk = k0 + u;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < NC; ++c) {
         int j = jb + (c / CP) * 4 * EL + (l16 >> 2) * EL + 4 * (c % CP) + (l16 & 3);
         j = j < a.width ? j : a.width - 1;
-        wf[u][c] = load_frag<E, VECW>(W + (int64_t)j * in.ldw, kk * KF + kc, in.ldw, wend);
+        wf[u][c] = load_frag<E, VECW>(W + (int64_t)j * in.ldw, (k0 + u) * KF + kc, in.ldw, wend);
       }
-      // (steps past the adapter's ranks: W is zero, T another's or none)
-      const bool tin = kk * KF < in.ldw;
+  };
+  load_w(0);
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+  for (int i = 0; i < RT; ++i) *reinterpret_cast<f32x2*>(&tl[i * 512 + tid * 2]) = t[i];
+  __syncthreads();
+  if (jb >= a.width) return;
+  f32x4 acc[NC][2];
 #pragma unroll
-        for (int q = 0; q < CP; ++q)
-          t[u][s][q] = tin ? *reinterpret_cast<const f32x4*>(T + (kk * 2 + s) * TS + 4 * q) : f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int p = 1; p < a.parts; ++p)
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int q = 0; q < CP; ++q)
-            if (tin) t[u][s][q] += *reinterpret_cast<const f32x4*>(T + p * a.tiles * size + (kk * 2 + s) * TS + 4 * q);
+  for (int c = 0; c < NC; ++c) acc[c][0] = acc[c][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int k0 = 0; k0 < NK; k0 += KU) {
+    if (k0 > 0) {
+      if (k0 * KF >= in.ldw) break;
+      load_w(k0);
     }
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
+      // steps past the adapter's ranks: W is zero, T was never written
+      if (k0 + u > 0 && (k0 + u) * KF >= in.ldw) continue;
       uint4 tf[2][NP];
+      // PACK: lane groups 0, 1 take half 0 of the tile's tokens, 2, 3 half 1
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < (PACK ? 1 : 2); ++s) {
+        const float* src = tl + (((k0 + u) * 2 + s) * 64 + lane) * EL;
         if constexpr (BF) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = t[u][s][e >> 2][e & 3];
+          const f32x4 f0 = *reinterpret_cast<const f32x4*>(src), f1 = *reinterpret_cast<const f32x4*>(src + 4);
+          const float f[8] = {f0[0], f0[1], f0[2], f0[3], f1[0], f1[1], f1[2], f1[3]};
           uint4 hi, lo;
           split8(f, hi, lo);
           if constexpr (PACK) {
-            const bool first = g < 2;
-            tf[s][0] = make_uint4(first ? hi.x : lo.x, first ? hi.y : lo.y, first ? hi.z : lo.z, first ? hi.w : lo.w);
+            // lanes < 32: hi of a half, lanes >= 32: its lo
+            tf[0][0] = hi;
+            tf[1][0] = lo;
+            swap32(tf[0][0], tf[1][0]);
           } else {
             tf[s][0] = hi;
             tf[s][NP - 1] = lo;
           }
         } else {
-          tf[s][0] = __builtin_bit_cast(uint4, t[u][s][0]);
+          tf[s][0] = *reinterpret_cast<const uint4*>(src);
         }
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -830,9 +880,9 @@ __global__ __launch_bounds__(256) void adapter_reduce_kernel(const ReduceArgs a)
   }
 }
 
-__global__ __launch_bounds__(512) void adapter_list_kernel(const AdSegs seg, const ListArgs lists) {
-  __shared__ int cnt[8];
-  build_list<512>(seg, lists, blockIdx.x, cnt);
+__global__ __launch_bounds__(256) void adapter_list_kernel(const AdSegs seg, const ListArgs lists) {
+  __shared__ int cnt[4];
+  build_list<256>(seg, lists, blockIdx.x, cnt);
 }
 
 }  // namespace poetx
@@ -890,8 +940,9 @@ int check_rows(const char* name, const void* p, int64_t ld, int64_t width, int32
 struct AdPlan {
   int64_t tiles;           // tile indices of a call
   int rpmax, run, runs, slots, groups;
-  int rt, rgroups, parts;  // shrink: rank tiles of a workgroup, their groups, parts of the width
-  float *T, *U, *F, *part[2];   // rows of T and U; frags of the expand's operand
+  int rt, rgroups, pw;     // shrink: rank tiles of a workgroup, their groups, columns of a part
+  int parts[2];            // of x and of dy
+  float *F[2], *T, *U, *part[2];   // frags of T and U, their sums in rows, the gradients' partial sums
   void* At;
   AdInfo* info;
   int4* list;
@@ -906,17 +957,18 @@ AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd,
   const bool f32 = s->dtype == POETX_F32;
   p.tiles = N / AD_T + nseg;
   p.rpmax = pad_rank(s->max_rank, s->max_rank);
-  // few tiles: the ranks, then (forward) the width, are shared out over more workgroups
+  // the shrink's parts: about 1024 workgroups, of 512 columns at least; where
+  // these are too few still, the ranks are shared out as well (x is then read again)
   const int rt_all = p.rpmax / 16;
   p.rt = rt_all < 4 ? ceil_rt(rt_all) : 4;
   auto groups = [&](int rt) { return (rt_all + rt - 1) / rt; };
-  while (p.rt > 1 && p.tiles * (bwd ? 2 : 1) * groups(p.rt) < 512) p.rt /= 2;
+  const int64_t widths = s->n + (bwd ? s->m : 0);
+  int64_t pw = (p.tiles * groups(p.rt) * widths / 1024 + 511) / 512 * 512;
+  p.pw = (int)(pw < 512 ? 512 : pw > 32768 ? 32768 : pw);
+  p.parts[0] = (int)((s->n + p.pw - 1) / p.pw);
+  p.parts[1] = bwd ? (int)((s->m + p.pw - 1) / p.pw) : 0;
+  while (p.rt > 1 && p.tiles * groups(p.rt) * (p.parts[0] + p.parts[1]) < 512) p.rt /= 2;
   p.rgroups = groups(p.rt);
-  p.parts = 1;
-  if (!bwd) {
-    const int64_t steps = (s->n + (f32 ? 31 : 63)) / (f32 ? 32 : 64);
-    while (p.parts < 8 && p.tiles * p.rgroups * p.parts < 256 && steps >= 16 * p.parts) p.parts *= 2;
-  }
   size_t off = 0;
   auto take = [&](size_t bytes) -> char* {
     off = (off + kWsAlign - 1) / kWsAlign * kWsAlign;
@@ -926,8 +978,9 @@ AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd,
   };
   const size_t tbytes = (size_t)p.tiles * p.rpmax * AD_T * sizeof(float);
   p.info = reinterpret_cast<AdInfo*>(take((size_t)p.tiles * sizeof(AdInfo)));
-  p.F = reinterpret_cast<float*>(take(p.parts * tbytes));
+  p.F[0] = reinterpret_cast<float*>(take(p.parts[0] * tbytes));
   if (bwd) {
+    p.F[1] = reinterpret_cast<float*>(take(p.parts[1] * tbytes));
     p.T = reinterpret_cast<float*>(take(tbytes));
     p.U = reinterpret_cast<float*>(take(tbytes));
     p.At = take((size_t)s->rows * s->n * (f32 ? 4 : 2));
@@ -951,21 +1004,27 @@ AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd,
   return p;
 }
 
+// x workgroups of each of `count` tiles (or more)
+dim3 tile_grid(int64_t x, int64_t count) {
+  return dim3((unsigned)x, (unsigned)(count < TILES_Y ? count : TILES_Y), (unsigned)((count + TILES_Y - 1) / TILES_Y));
+}
+
 AdSegs segs_of(const poetx_adapters* s, const int32_t* start, const int32_t* which, int32_t nseg, int64_t N) {
   return AdSegs{start, which, nseg, s->count, (int32_t)N};
 }
 
 template <typename E>
-void launch_shrink(ShrinkArgs a, const AdPlan& p, int jobs, int extra, bool vec, hipStream_t s) {
+void launch_shrink(ShrinkArgs a, const AdPlan& p, int64_t extra, bool vec, hipStream_t s) {
   a.rpmax = p.rpmax;
   a.tiles = (int)p.tiles;
-  a.parts = p.parts;
+  a.info = p.info;
+  a.pw = p.pw;
   a.groups = p.rgroups;
-  const dim3 grid((unsigned)(p.tiles + extra), (unsigned)(jobs * p.rgroups * p.parts));
+  const dim3 grid = tile_grid((p.parts[0] + p.parts[1]) * p.rgroups, p.tiles + extra);
 #define POETX_RT(R) \
   case R: \
-    if (vec) hipLaunchKernelGGL((adapter_shrink_kernel<E, R, true>), grid, dim3(512), 0, s, a); \
-    else hipLaunchKernelGGL((adapter_shrink_kernel<E, R, false>), grid, dim3(512), 0, s, a); \
+    if (vec) hipLaunchKernelGGL((adapter_shrink_kernel<E, R, true>), grid, dim3(64 * SHRINK_WAVES), 0, s, a); \
+    else hipLaunchKernelGGL((adapter_shrink_kernel<E, R, false>), grid, dim3(64 * SHRINK_WAVES), 0, s, a); \
     break;
   switch (p.rt) { POETX_RT(1) POETX_RT(2) POETX_RT(4) }
 #undef POETX_RT
@@ -981,14 +1040,13 @@ template <typename E>
 void launch_expand(ExpandArgs a, const AdPlan& p, bool vecw, hipStream_t s) {
   const size_t es = sizeof(E);
   const bool vecy = al16(a.Y) && a.ldy * es % 16 == 0 && a.width * es % 16 == 0;
-  a.T = p.F;
   a.info = p.info;
   a.rpmax = p.rpmax;
   a.tiles = (int)p.tiles;
-  a.parts = p.parts;
-  const dim3 grid((unsigned)((a.width + 255) / 256), (unsigned)(p.tiles < EXPAND_Y ? p.tiles : EXPAND_Y),
-                  (unsigned)((p.tiles + EXPAND_Y - 1) / EXPAND_Y));
-  switch (ceil_rt(p.rpmax / 16)) {
+  const int rt = ceil_rt(p.rpmax / 16), wide = 64 * expand_nc(rt);
+  a.cols = a.Y ? (a.width + wide - 1) / wide : 0;
+  const dim3 grid = tile_grid(a.cols + (a.rows[0] ? 2 : 0), p.tiles);
+  switch (rt) {
     case 1: expand<E, 1>(a, grid, vecy, vecw, s); break;
     case 2: expand<E, 2>(a, grid, vecy, vecw, s); break;
     case 4: expand<E, 4>(a, grid, vecy, vecw, s); break;
@@ -1012,17 +1070,16 @@ int forward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, in
   {
     HostTimer tm(s, "adapter_shrink", flops * set->n, (double)seg.N * set->n * es);
     ShrinkArgs a{};
-    a.job[0] = ShrinkJob{X, nullptr, p.F, ldx, (int)set->n, 0};
-    a.info = p.info;
+    a.job[0] = ShrinkJob{X, p.F[0], ldx, (int)set->n, p.parts[0], 0};
     a.seg = seg;
     a.table = table;
     const bool vec = al16(X) && ldx * es % 16 == 0 && set->n * es % 16 == 0 && (set->layout & LAY_A16);
-    launch_shrink<E>(a, p, 1, 0, vec, s);
+    launch_shrink<E>(a, p, 0, vec, s);
   }
   {
     HostTimer tm(s, "adapter_expand", flops * set->m, 2.0 * seg.N * set->m * es);
     ExpandArgs a{};
-    a.Y = Y; a.ldy = ldy; a.width = (int)set->m;
+    a.Y = Y; a.ldy = ldy; a.width = (int)set->m; a.T = p.F[0]; a.parts = p.parts[0];
     launch_expand<E>(a, p, (set->layout & LAY_B16) != 0, s);
   }
   return host_check_launch("adapters forward");
@@ -1039,22 +1096,30 @@ int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, i
   const bool yvec = al16(dY) && lddy * es % 16 == 0 && m * es % 16 == 0;
   const ListArgs lists{p.list, p.offs, (int)p.tiles};
   if (p.tiles == 0) {
-    hipLaunchKernelGGL(adapter_list_kernel, dim3((unsigned)set->count), dim3(512), 0, s, seg, lists);
+    hipLaunchKernelGGL(adapter_list_kernel, dim3((unsigned)set->count), dim3(256), 0, s, seg, lists);
   } else {
     {
       HostTimer tm(s, "adapter_shrink", flops * (m + n), (double)seg.N * (m + n) * es);
       ShrinkArgs a{};
-      a.job[0] = ShrinkJob{X, p.T, nullptr, ldx, n, 0};
-      a.job[1] = ShrinkJob{dY, p.U, dX ? p.F : nullptr, lddy, m, 1};
+      a.job[0] = ShrinkJob{X, p.F[0], ldx, n, p.parts[0], 0};
+      a.job[1] = ShrinkJob{dY, p.F[1], lddy, m, p.parts[1], 1};
       a.seg = seg;
       a.table = table;
-      a.info = p.info;
       a.lists = lists;
       // columns of A turned by a workgroup: a power of two whose ranks fit the LDS
       int tw = 64;
-      while (tw > 16 && (size_t)tw * (set->max_rank + 3) * es > TURN_LDS) tw /= 2;
+      while (tw > 8 && (size_t)tw * (set->max_rank + 3) * es > TURN_LDS) tw /= 2;
       a.turn = TurnArgs{dX ? p.At : nullptr, n, (n + tw - 1) / tw, tw};
-      launch_shrink<E>(a, p, 2, set->count * (1 + (dX ? a.turn.per : 0)), xvec && yvec && set->layout == (LAY_A16 | LAY_B16), s);
+      launch_shrink<E>(a, p, (int64_t)set->count * (1 + (dX ? a.turn.per : 0)), xvec && yvec && set->layout == (LAY_A16 | LAY_B16),
+                       s);
+    }
+    {
+      HostTimer tm(s, "adapter_expand", flops * n, 2.0 * seg.N * n * es);
+      ExpandArgs a{};
+      a.Y = dX; a.ldy = lddx; a.width = n; a.T = p.F[1]; a.parts = p.parts[1];
+      a.F[0] = p.F[0]; a.F[1] = p.F[1]; a.rows[0] = p.T; a.rows[1] = p.U;
+      a.fparts[0] = p.parts[0]; a.fparts[1] = p.parts[1];
+      launch_expand<E>(a, p, true, s);
     }
     {
       HostTimer tm(s, "adapter_outer", 2 * flops * (m + n), (double)seg.N * (m + n) * es);
@@ -1068,12 +1133,6 @@ int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, i
       if (p.rpmax == 16) outer<E, 1>(a, grid, xvec && yvec, s);
       else if (p.rpmax == 32) outer<E, 2>(a, grid, xvec && yvec, s);
       else outer<E, 4>(a, grid, xvec && yvec, s);
-    }
-    if (dX) {
-      HostTimer tm(s, "adapter_expand", flops * n, 2.0 * seg.N * n * es);
-      ExpandArgs a{};
-      a.Y = dX; a.ldy = lddx; a.width = n;
-      launch_expand<E>(a, p, true, s);
     }
   }
   {
