@@ -229,6 +229,9 @@ def stream_handle(stream):
     given as an int, or None (torch's current stream)."""
     if stream is None:
         import torch
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if get is not None:     # without the Stream object (3 us less)
+            return get(torch.cuda.current_device())
         return int(torch.cuda.current_stream().cuda_stream)
     if hasattr(stream, "cuda_stream"):
         return int(stream.cuda_stream)

@@ -516,22 +516,6 @@ __device__ __forceinline__ uint4 add_frag(uint4 y, const float* v) {
 // MFMAs across a wave's columns, 16 columns each:
 constexpr int expand_nc(int rt) { return rt == 1 ? 8 : 4; }
 
-template <typename E>
-__device__ __forceinline__ void sum_rows(const ExpandArgs& a, int64_t w, int job) {
-  constexpr int EL = El<E>::EL, KF = El<E>::KF;
-  const int64_t size = (int64_t)a.rpmax * AD_T;
-  const int lanes = a.rpmax < KF ? 16 * (a.rpmax / EL) : 64;
-  const float* F = a.F[job] + w * size;
-  float* rows = a.rows[job] + w * size;
-  for (int i = threadIdx.x; i < (int)size; i += 256) {
-    float v = F[i];
-#pragma unroll 4
-    for (int p = 1; p < a.fparts[job]; ++p) v += F[p * a.tiles * size + i];
-    const int e = i % EL, lane = i / EL % lanes, s = i / EL / lanes & 1, kk = i / EL / lanes >> 1;
-    rows[(kk * KF + (lane >> 4) * EL + e) * AD_T + 16 * s + (lane & 15)] = v;
-  }
-}
-
 template <typename E, int RT, bool VECY, bool VECW>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a) {
   constexpr int EL = El<E>::EL, KF = El<E>::KF;
@@ -549,36 +533,47 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a)
   if (w >= a.tiles) return;
   const AdInfo in = a.info[w];
   if (in.rows == 0) return;
-  if ((int)blockIdx.x >= a.cols) {
-    sum_rows<E>(a, w, blockIdx.x - a.cols);
-    return;
-  }
-  const int jb = (blockIdx.x * 4 + wave) * 16 * NC;
   // T, its parts added: two floats a thread and rank tile
+  const int job = (int)blockIdx.x - a.cols;   // >= 0: a sum for the gradients
   const int64_t size = (int64_t)a.rpmax * AD_T;
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   f32x2 t[RT];
   {
-    const float* T = a.T + w * size + tid * 2;
+    const float* T = (job >= 0 ? a.F[job] : a.T) + w * size + tid * 2;
+    const int parts = job >= 0 ? a.fparts[job] : a.parts;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
       t[i] = 16 * i < a.rpmax ? *reinterpret_cast<const f32x2*>(T + i * 512) : f32x2{0.f, 0.f};
     // four parts' loads at a time
-    for (int p = 1; p < a.parts; p += 4) {
+    for (int p = 1; p < parts; p += 4) {
       f32x2 q[4][RT];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int i = 0; i < RT; ++i)
-          if (p + k < a.parts && 16 * i < a.rpmax)
+          if (p + k < parts && 16 * i < a.rpmax)
             q[k][i] = *reinterpret_cast<const f32x2*>(T + (p + k) * a.tiles * size + i * 512);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int i = 0; i < RT; ++i)
-          if (p + k < a.parts) t[i] += q[k][i];
+          if (p + k < parts) t[i] += q[k][i];
     }
   }
+  if (job >= 0) {
+    float* rows = a.rows[job] + w * size;
+    const int lanes = PACK ? 32 : 64;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = i * 512 + tid * 2 + h;
+        const int e = k % EL, ln = k / EL % lanes, s = k / EL / lanes & 1, kk = k / EL / lanes >> 1;
+        if (16 * i < a.rpmax) rows[(kk * KF + (ln >> 4) * EL + e) * AD_T + 16 * s + (ln & 15)] = t[i][h];
+      }
+    return;
+  }
+  const int jb = (blockIdx.x * 4 + wave) * 16 * NC;
   // element e of contraction step kk: rank kk KF + kc + e
   const int kc = PACK ? 8 * (g & 1) : g * EL;
   const E* W = static_cast<const E*>(in.W);
@@ -693,64 +688,38 @@ struct OuterArgs {
   OuterJob job[2];
   const int4* list;
   const int32_t* offs;
-  int count, rpmax, run, groups;   // run: list entries of a workgroup; groups of 64 ranks
+  int count, rpmax, run, slabs0;   // run: list entries of a workgroup; slabs0: slabs of job 0
   int N;
 };
 
-// Wave: one slab of columns (16 lanes x EL), every list entry of the run.
-// Lane (g, c) loads EL neighbouring columns of its tokens; the MFMA for
-// element e takes column EL c + e as its row c.  bf16: eight tokens a lane
-// (8 g + i), gathered into operands of eight tokens by byte permutes; fp32:
-// MFMA step i takes token 4 i + g.  Partial sums of one adapter within a run
-// go to slot run + adapter (each run begins where the one before it ended, so
-// no two pairs share a slot); a second kernel adds an adapter's slots in order.
-template <typename E, int RT, bool VEC>
+// A workgroup takes a slab of columns (16 lanes x EL), 16 ranks and a run of
+// list entries, every fourth a wave; the waves' sums of one adapter are added
+// in LDS.  (With 64 ranks a workgroup x is read once, but one wave fills a
+// SIMD's registers: rank 64, 2001 tokens 27.6 us against 17.3 us.)
+// Lane (g, c) loads EL neighbouring columns of its tokens; the MFMA for element
+// e takes column EL c + e as its row c.  bf16: eight tokens a lane (8 g + i),
+// gathered into operands of eight tokens by byte permutes; fp32: MFMA step i
+// takes token 4 i + g.  Sums of an adapter within a run go to slot run + adapter
+// (a run begins where the one before it ended, so no two pairs share a
+// slot); a second kernel adds an adapter's slots in order.  A slot is written
+// and read as fp32, rank x (n + m): with a run for each wave those bytes
+// outweighed the activations (the same case: 32.8 us).
+template <typename E, bool VEC>
 __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
-  constexpr int EL = El<E>::EL;
+  constexpr int EL = El<E>::EL, COLS = 16 * EL, LD = COLS + 4;
   constexpr bool BF = EL == 8;
-  const int jz = blockIdx.z / a.groups, grp = blockIdx.z % a.groups;
+  __shared__ __align__(16) float red[4][16 * LD];
+  int bx = blockIdx.x;
+  const int jz = bx >= a.slabs0;
+  if (jz) bx -= a.slabs0;
   const OuterJob& J = a.job[jz];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rank0 = blockIdx.z * 16;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int cb = (blockIdx.x * 4 + wave) * 16 * EL;
-  if (cb >= J.width) return;
-  const int col = cb + l16 * EL;
+  const int cb = bx * COLS, col = cb + l16 * EL;
   const int total = a.offs[a.count];
   int e0 = blockIdx.y * a.run, e1 = e0 + a.run;
   if (e1 > total) e1 = total;
-  if (e0 >= e1) return;
-  f32x4 acc[EL][RT];
-  auto clear = [&]() {
-#pragma unroll
-    for (int e = 0; e < EL; ++e)
-#pragma unroll
-      for (int i = 0; i < RT; ++i) acc[e][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  };
-  auto flush = [&](int adapter) {
-    float* P = J.part + (int64_t)(blockIdx.y + adapter) * a.rpmax * J.width;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int rank = grp * 64 + 16 * i + l16;
-      if (rank >= a.rpmax) continue;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = cb + (4 * g + q) * EL;
-        float* dst = P + (int64_t)rank * J.width + c;
-        if (VEC) {
-          if (c < J.width) {
-#pragma unroll
-            for (int h = 0; h < EL / 4; ++h)
-              *reinterpret_cast<f32x4*>(dst + 4 * h) =
-                  f32x4{acc[4 * h][i][q], acc[4 * h + 1][i][q], acc[4 * h + 2][i][q], acc[4 * h + 3][i][q]};
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < EL; ++e)
-            if (c + e < J.width) dst[e] = acc[e][i][q];
-        }
-      }
-    }
-  };
   const E* xend = static_cast<const E*>(J.X) + (int64_t)(a.N - 1) * J.ldx + J.width;
   auto load = [&](uint4 (&x)[8], const int4& en) {
     const E* X = static_cast<const E*>(J.X) + (int64_t)en.x * J.ldx;
@@ -761,27 +730,28 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
       x[i] = t < en.y ? load_frag<E, VEC>(X + (int64_t)t * J.ldx, col, J.width, xend) : make_uint4(0, 0, 0, 0);
     }
   };
-  clear();
-  int4 en = a.list[e0];
-  int cur = en.z;
-  uint4 x[8], nx[8];
-  load(x, en);
-  for (int p = e0;;) {
-    const bool more = p + 1 < e1;
-    int4 en2 = en;
-    if (more) {
-      en2 = a.list[p + 1];
-      load(nx, en2);   // on its way while this tile is multiplied
-    }
-    const float* T = J.T + (int64_t)en.w * a.rpmax * AD_T;
-    if constexpr (BF) {
-      uint4 op[8];   // operand e: column e of the lane, eight tokens
-      transpose8(x, op);
+  while (e0 < e1) {
+    const int adapter = a.list[e0].z;
+    const int own = a.offs[adapter + 1], end = own < e1 ? own : e1;
+    f32x4 acc[EL];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const int rank = grp * 64 + 16 * i + l16;
-        const float* tr = T + (rank < a.rpmax ? rank : 0) * AD_T + 8 * g;
-        const f32x4 f0 = *reinterpret_cast<const f32x4*>(tr), f1 = *reinterpret_cast<const f32x4*>(tr + 4);
+    for (int e = 0; e < EL; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint4 x[8], nx[8];
+    int p = e0 + wave;
+    int4 en = make_int4(0, 0, 0, 0);
+    if (p < end) {
+      en = a.list[p];
+      load(x, en);
+    }
+    while (p < end) {
+      int4 en2 = en;
+      if (p + 4 < end) {
+        en2 = a.list[p + 4];
+        load(nx, en2);   // on its way while this tile is multiplied
+      }
+      const float* T = J.T + ((int64_t)en.w * a.rpmax + rank0 + l16) * AD_T;
+      if constexpr (BF) {
+        const f32x4 f0 = *reinterpret_cast<const f32x4*>(T + 8 * g), f1 = *reinterpret_cast<const f32x4*>(T + 8 * g + 4);
         const float f[8] = {f0[0], f0[1], f0[2], f0[3], f1[0], f1[1], f1[2], f1[3]};
         // three bf16 values keep all 24 bits of T: the gradients are fp32
         float rest[8];
@@ -791,40 +761,47 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) rest[e] = f[e] - (float)hb[e] - (float)lb[e];
         split8(rest, l2, none);
+        uint4 op[8];   // operand e: column e of the lane, eight tokens
+        transpose8(x, op);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          acc[e][i] = El<E>::mma(op[e], h, acc[e][i]);
-          acc[e][i] = El<E>::mma(op[e], l, acc[e][i]);
-          acc[e][i] = El<E>::mma(op[e], l2, acc[e][i]);
+          acc[e] = El<E>::mma(op[e], h, acc[e]);
+          acc[e] = El<E>::mma(op[e], l, acc[e]);
+          acc[e] = El<E>::mma(op[e], l2, acc[e]);
         }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const int rank = grp * 64 + 16 * i + l16;
-        const float* tr = T + (rank < a.rpmax ? rank : 0) * AD_T + g;
+      } else {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-          const float f = tr[4 * s];
-          acc[0][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[s].x), f, acc[0][i], 0, 0, 0);
-          acc[1][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[s].y), f, acc[1][i], 0, 0, 0);
-          acc[2][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[s].z), f, acc[2][i], 0, 0, 0);
-          acc[3][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[s].w), f, acc[3][i], 0, 0, 0);
+          const float f = T[4 * s + g];
+          acc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[s].x), f, acc[0], 0, 0, 0);
+          acc[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[s].y), f, acc[1], 0, 0, 0);
+          acc[2] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[s].z), f, acc[2], 0, 0, 0);
+          acc[3] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[s].w), f, acc[3], 0, 0, 0);
         }
       }
-    }
-    if (!more) break;
-    if (en2.z != cur) {
-      flush(cur);
-      clear();
-      cur = en2.z;
-    }
-    ++p;
-    en = en2;
+      p += 4;
+      en = en2;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = nx[i];
+      for (int i = 0; i < 8; ++i) x[i] = nx[i];
+    }
+    // the waves' sums; element e of lane (g, rank l16), row q: column (4 g + q) EL + e
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < EL; e += 4)
+        *reinterpret_cast<f32x4*>(&red[wave][l16 * LD + (4 * g + q) * EL + e]) =
+            f32x4{acc[e][q], acc[e + 1][q], acc[e + 2][q], acc[e + 3][q]};
+    __syncthreads();
+    float* P = J.part + ((int64_t)(blockIdx.y + adapter) * a.rpmax + rank0) * J.width + cb;
+    const int c = tid % COLS;
+#pragma unroll
+    for (int r = tid / COLS; r < 16; r += 256 / COLS) {
+      const float v = (red[0][r * LD + c] + red[1][r * LD + c]) + (red[2][r * LD + c] + red[3][r * LD + c]);
+      if (cb + c < J.width) P[(int64_t)r * J.width + c] = v;
+    }
+    __syncthreads();
+    e0 = end;
   }
-  flush(cur);
 }
 
 struct ReduceArgs {
@@ -939,7 +916,7 @@ int check_rows(const char* name, const void* p, int64_t ld, int64_t width, int32
 
 struct AdPlan {
   int64_t tiles;           // tile indices of a call
-  int rpmax, run, runs, slots, groups;
+  int rpmax, run, runs, slots, slabs[2];
   int rt, rgroups, pw;     // shrink: rank tiles of a workgroup, their groups, columns of a part
   int parts[2];            // of x and of dy
   float *F[2], *T, *U, *part[2];   // frags of T and U, their sums in rows, the gradients' partial sums
@@ -987,14 +964,11 @@ AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd,
     p.list = reinterpret_cast<int4*>(take((size_t)p.tiles * sizeof(int4)));
     p.offs = reinterpret_cast<int32_t*>(take((size_t)(s->count + 1) * sizeof(int32_t)));
     // runs of tiles: about 512 workgroups over both gradients
-    p.groups = (p.rpmax + 63) / 64;
-    const int64_t slab = 4 * 16 * (f32 ? 4 : 8);
-    const int64_t x = ((s->m + slab - 1) / slab + (s->n + slab - 1) / slab) * p.groups;
-    int64_t runs = 512 / x;
-    if (runs < 1) runs = 1;
-    if (runs > p.tiles) runs = p.tiles > 0 ? p.tiles : 1;
-    p.run = (int)((p.tiles + runs - 1) / runs);
-    if (p.run < 1) p.run = 1;
+    const int64_t cols = f32 ? 64 : 128;
+    p.slabs[0] = (int)((s->n + cols - 1) / cols);
+    p.slabs[1] = (int)((s->m + cols - 1) / cols);
+    const int64_t run = p.tiles * (p.slabs[0] + p.slabs[1]) * rt_all / 512;
+    p.run = (int)(run < 1 ? 1 : run);
     p.runs = (int)((p.tiles + p.run - 1) / p.run);
     p.slots = p.runs + s->count;
     p.part[0] = reinterpret_cast<float*>(take((size_t)p.slots * p.rpmax * s->n * sizeof(float)));
@@ -1053,12 +1027,6 @@ void launch_expand(ExpandArgs a, const AdPlan& p, bool vecw, hipStream_t s) {
     case 8: expand<E, 8>(a, grid, vecy, vecw, s); break;
     case 16: expand<E, 16>(a, grid, vecy, vecw, s); break;
   }
-}
-
-template <typename E, int RT>
-void outer(const OuterArgs& a, dim3 grid, bool vec, hipStream_t s) {
-  if (vec) hipLaunchKernelGGL((adapter_outer_kernel<E, RT, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((adapter_outer_kernel<E, RT, false>), grid, dim3(256), 0, s, a);
 }
 
 template <typename E>
@@ -1126,13 +1094,11 @@ int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, i
       OuterArgs a{};
       a.job[0] = OuterJob{X, p.U, p.part[0], ldx, n};
       a.job[1] = OuterJob{dY, p.T, p.part[1], lddy, m};
-      a.list = p.list; a.offs = p.offs; a.count = set->count; a.rpmax = p.rpmax; a.run = p.run; a.groups = p.groups;
+      a.list = p.list; a.offs = p.offs; a.count = set->count; a.rpmax = p.rpmax; a.run = p.run; a.slabs0 = p.slabs[0];
       a.N = seg.N;
-      const int slab = 4 * 16 * El<E>::EL, wide = m > n ? m : n;
-      const dim3 grid((unsigned)((wide + slab - 1) / slab), (unsigned)p.runs, (unsigned)(2 * p.groups));
-      if (p.rpmax == 16) outer<E, 1>(a, grid, xvec && yvec, s);
-      else if (p.rpmax == 32) outer<E, 2>(a, grid, xvec && yvec, s);
-      else outer<E, 4>(a, grid, xvec && yvec, s);
+      const dim3 grid((unsigned)(p.slabs[0] + p.slabs[1]), (unsigned)p.runs, (unsigned)(p.rpmax / 16));
+      if (xvec && yvec) hipLaunchKernelGGL((adapter_outer_kernel<E, true>), grid, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((adapter_outer_kernel<E, false>), grid, dim3(256), 0, s, a);
     }
   }
   {
