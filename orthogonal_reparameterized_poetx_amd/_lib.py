@@ -460,14 +460,14 @@ def adapters_workspace_bytes(aset, N, nseg, op):
 
 def poetx_adapters_forward(aset, seg_start, seg_adapter, nseg, X, ldx, N, Y, ldy, ws, stream=None):
     _check("poetx_adapters_forward", lib().poetx_adapters_forward(
-        ctypes.byref(aset), _ptr(seg_start), _ptr(seg_adapter), int(nseg), _ptr(X), int(ldx), int(N), _ptr(Y),
-        int(ldy), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+        ctypes.byref(aset), seg_start.data_ptr(), seg_adapter.data_ptr(), nseg, X.data_ptr(), ldx, N, Y.data_ptr(),
+        ldy, ws.data_ptr(), ws.numel(), stream_handle(stream)))
 
 
 def poetx_adapters_backward(aset, seg_start, seg_adapter, nseg, X, ldx, dY, lddy, N, dX, lddx, ws, stream=None):
     _check("poetx_adapters_backward", lib().poetx_adapters_backward(
-        ctypes.byref(aset), _ptr(seg_start), _ptr(seg_adapter), int(nseg), _ptr(X), int(ldx), _ptr(dY), int(lddy),
-        int(N), _ptr(dX), int(lddx), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+        ctypes.byref(aset), seg_start.data_ptr(), seg_adapter.data_ptr(), nseg, X.data_ptr(), ldx, dY.data_ptr(),
+        lddy, N, _addr(dX), lddx, ws.data_ptr(), ws.numel(), stream_handle(stream)))
 
 
 def param_table(params):
@@ -489,18 +489,18 @@ def grad_norm_workspace_bytes(pset):
 
 
 def poetx_grad_norm(pset, max_norm, out, ws, stream=None):
-    _check("poetx_grad_norm", lib().poetx_grad_norm(ctypes.byref(pset), float(max_norm), _ptr(out), _ptr(ws),
-                                                    ws.numel() if ws is not None else 0, _stream(stream)))
+    _check("poetx_grad_norm", lib().poetx_grad_norm(ctypes.byref(pset), max_norm, out.data_ptr(), ws.data_ptr(),
+                                                    ws.numel(), stream_handle(stream)))
 
 
 def poetx_adamw_step(pset, state, hyper, step, coef=None, stream=None):
     _check("poetx_adamw_step", lib().poetx_adamw_step(ctypes.byref(pset), ctypes.byref(state), ctypes.byref(hyper),
-                                                      int(step), _ptr(coef), _stream(stream)))
+                                                      step, _addr(coef), stream_handle(stream)))
 
 
 def poetx_adamw_moments(pset, state, m_out, v_out, stream=None):
-    _check("poetx_adamw_moments", lib().poetx_adamw_moments(ctypes.byref(pset), ctypes.byref(state), _ptr(m_out),
-                                                            _ptr(v_out), _stream(stream)))
+    _check("poetx_adamw_moments", lib().poetx_adamw_moments(ctypes.byref(pset), ctypes.byref(state), _addr(m_out),
+                                                            _addr(v_out), stream_handle(stream)))
 
 
 def timing_enable(on):

@@ -38,7 +38,7 @@ class AdapterSet:
             self._check("A[%d]" % i, a, (r, self.n), self.dtype)
             self._check("B[%d]" % i, b, (self.m, r), self.dtype)
         self.dA, self.dB = self._grads("dA", dA, self.A), self._grads("dB", dB, self.B)
-        self._ws = {}
+        self._ws, self._need = {}, {}     # workspaces by op; their sizes by (op, tokens, segments)
         self._make_table()
 
     def _check(self, name, t, shape, dtype):
@@ -86,7 +86,11 @@ class AdapterSet:
         return seg_adapter.numel()
 
     def workspace(self, op, N, nseg):
-        need = L.adapters_workspace_bytes(self.aset, N, nseg, op)
+        need = self._need.get((op, N, nseg))
+        if need is None:
+            if len(self._need) > 4096:
+                self._need.clear()
+            need = self._need[op, N, nseg] = L.adapters_workspace_bytes(self.aset, N, nseg, op)
         ws = self._ws.get(op)
         if ws is None or ws.numel() < need:
             ws = self._ws[op] = L.make_workspace(need, self.device)

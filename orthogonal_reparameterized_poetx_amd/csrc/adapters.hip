@@ -516,16 +516,100 @@ __device__ __forceinline__ uint4 add_frag(uint4 y, const float* v) {
 // MFMAs across a wave's columns, 16 columns each:
 constexpr int expand_nc(int rt) { return rt == 1 ? 8 : 4; }
 
+// T's operands of contraction step kk from LDS; PACK: lane groups 0, 1 hold half
+// 0 of the tile's tokens, 2, 3 half 1
+template <typename E, int RT>
+struct Operands {
+  static constexpr int EL = El<E>::EL, KF = El<E>::KF;
+  static constexpr bool BF = EL == 8, PACK = BF && RT == 1;   // PACK: 16 ranks, hi and lo side by side in one MFMA
+  static constexpr int NK = PACK ? 1 : RT * 16 / KF, NP = BF && !PACK ? 2 : 1;
+  // element e of step kk: rank kk KF + rank0 + e
+  static __device__ __forceinline__ int rank0(int g) { return PACK ? 8 * (g & 1) : g * EL; }
+  static __device__ __forceinline__ void load(const float* tl, int kk, int lane, uint4 (&tf)[2][NP]) {
+#pragma unroll
+    for (int s = 0; s < (PACK ? 1 : 2); ++s) {
+      const float* src = tl + ((kk * 2 + s) * 64 + lane) * EL;
+      if constexpr (BF) {
+        const f32x4 f0 = *reinterpret_cast<const f32x4*>(src), f1 = *reinterpret_cast<const f32x4*>(src + 4);
+        const float f[8] = {f0[0], f0[1], f0[2], f0[3], f1[0], f1[1], f1[2], f1[3]};
+        uint4 hi, lo;
+        split8(f, hi, lo);
+        if constexpr (PACK) {
+          // lanes < 32: hi of a half, lanes >= 32: its lo
+          tf[0][0] = hi;
+          tf[1][0] = lo;
+          swap32(tf[0][0], tf[1][0]);
+        } else {
+          tf[s][0] = hi;
+          tf[s][NP - 1] = lo;
+        }
+      } else {
+        tf[s][0] = *reinterpret_cast<const uint4*>(src);
+      }
+    }
+  }
+};
+
+// a wave's columns of a tile of Y: column of MFMA c, the pieces as read ahead,
+// and the update; y[s]: the lane's token of half s at its first column, `left`
+// columns before the width's end
+template <typename E, int NC, bool VECY>
+struct Columns {
+  static constexpr int EL = El<E>::EL, CP = EL / 4, NH = NC / CP;   // CP: MFMAs of a piece, NH: pieces of a lane and token
+  E* y[2];
+  int left, rows, l16;
+  uint4 old[2][NH];
+  static __device__ __forceinline__ int col(int c, int l16) {
+    return (c / CP) * 4 * EL + (l16 >> 2) * EL + 4 * (c % CP) + (l16 & 3);
+  }
+  __device__ __forceinline__ void init(void* Y, int64_t ldy, int t0, int rows_, int jb, int width, int lane) {
+    l16 = lane & 15;
+    rows = rows_;
+    const int j = jb + (lane >> 4) * EL;
+    left = width - j;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) y[s] = static_cast<E*>(Y) + (int64_t)(t0 + 16 * s + l16) * ldy + j;
+    if (VECY) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+          if (h * 4 * EL < left && 16 * s + l16 < rows) old[s][h] = gld16(y[s] + h * 4 * EL);
+    }
+  }
+  __device__ __forceinline__ void add(const f32x4 (&acc)[NC][2]) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (16 * s + l16 >= rows) continue;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        E* o = y[s] + h * 4 * EL;
+        const int n = left - h * 4 * EL;
+        float v[EL];
+#pragma unroll
+        for (int e = 0; e < EL; ++e) v[e] = acc[h * CP + (e >> 2)][s][e & 3];
+        if (VECY) {
+          if (n > 0) gst16(o, add_frag<E>(old[s][h], v));
+        } else if (n >= EL) {
+          gst16_u(o, add_frag<E>(gld16_u(o), v));
+        } else {
+#pragma unroll
+          for (int e = 0; e < EL; ++e)
+            if (e < n) {
+              if constexpr (EL == 8) o[e] = f32_to_bits(bits_to_f32(o[e]) + v[e]);
+              else o[e] += v[e];
+            }
+        }
+      }
+    }
+  }
+};
+
 template <typename E, int RT, bool VECY, bool VECW>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a) {
-  constexpr int EL = El<E>::EL, KF = El<E>::KF;
-  constexpr bool BF = EL == 8;
-  constexpr bool PACK = BF && RT == 1;   // 16 ranks: hi and lo side by side in one MFMA
-  constexpr int NK = PACK ? 1 : RT * 16 / KF;
-  constexpr int NP = BF && !PACK ? 2 : 1;
-  constexpr int NC = expand_nc(RT), CP = EL / 4;   // MFMAs of a wave, of a 16-byte piece
-  constexpr int NH = NC / CP;                      // 16-byte pieces of a lane and token
-  constexpr int KU = RT <= 4 ? NK : 1;   // contraction steps whose operands are in flight together
+  using Op = Operands<E, RT>;
+  constexpr int EL = El<E>::EL, KF = El<E>::KF, NK = Op::NK, NC = expand_nc(RT);
+  constexpr int KU = RT <= 4 ? NK : 1;   // contraction steps whose W is in flight together
   __shared__ __align__(16) float tl[RT * 512];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -562,7 +646,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a)
   }
   if (job >= 0) {
     float* rows = a.rows[job] + w * size;
-    const int lanes = PACK ? 32 : 64;
+    const int lanes = Op::PACK ? 32 : 64;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -574,29 +658,18 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a)
     return;
   }
   const int jb = (blockIdx.x * 4 + wave) * 16 * NC;
-  // element e of contraction step kk: rank kk KF + kc + e
-  const int kc = PACK ? 8 * (g & 1) : g * EL;
+  const int kc = Op::rank0(g);
   const E* W = static_cast<const E*>(in.W);
   const E* wend = W + (int64_t)a.width * in.ldw;
-  E* y[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) y[s] = static_cast<E*>(a.Y) + (int64_t)(in.t0 + 16 * s + l16) * a.ldy + jb + g * EL;
-  const int left = a.width - jb - g * EL;   // columns from the lane's first on
-  uint4 yv[2][NH];
-  if (VECY) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int h = 0; h < NH; ++h)
-        if (h * 4 * EL < left && 16 * s + l16 < in.rows) yv[s][h] = gld16(y[s] + h * 4 * EL);
-  }
+  Columns<E, NC, VECY> out;
+  out.init(a.Y, a.ldy, in.t0, in.rows, jb, a.width, lane);
   uint4 wf[KU][NC];
   auto load_w = [&](int k0) {
 #pragma unroll
     for (int u = 0; u < KU; ++u)
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        int j = jb + (c / CP) * 4 * EL + (l16 >> 2) * EL + 4 * (c % CP) + (l16 & 3);
+        int j = jb + out.col(c, l16);
         j = j < a.width ? j : a.width - 1;
         wf[u][c] = load_frag<E, VECW>(W + (int64_t)j * in.ldw, (k0 + u) * KF + kc, in.ldw, wend);
       }
@@ -619,61 +692,131 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a)
     for (int u = 0; u < KU; ++u) {
       // steps past the adapter's ranks: W is zero, T was never written
       if (k0 + u > 0 && (k0 + u) * KF >= in.ldw) continue;
-      uint4 tf[2][NP];
-      // PACK: lane groups 0, 1 take half 0 of the tile's tokens, 2, 3 half 1
-#pragma unroll
-      for (int s = 0; s < (PACK ? 1 : 2); ++s) {
-        const float* src = tl + (((k0 + u) * 2 + s) * 64 + lane) * EL;
-        if constexpr (BF) {
-          const f32x4 f0 = *reinterpret_cast<const f32x4*>(src), f1 = *reinterpret_cast<const f32x4*>(src + 4);
-          const float f[8] = {f0[0], f0[1], f0[2], f0[3], f1[0], f1[1], f1[2], f1[3]};
-          uint4 hi, lo;
-          split8(f, hi, lo);
-          if constexpr (PACK) {
-            // lanes < 32: hi of a half, lanes >= 32: its lo
-            tf[0][0] = hi;
-            tf[1][0] = lo;
-            swap32(tf[0][0], tf[1][0]);
-          } else {
-            tf[s][0] = hi;
-            tf[s][NP - 1] = lo;
-          }
-        } else {
-          tf[s][0] = *reinterpret_cast<const uint4*>(src);
-        }
-      }
+      uint4 tf[2][Op::NP];
+      Op::load(tl, k0 + u, lane, tf);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int p = 0; p < NP; ++p) acc[c][s] = El<E>::mma(wf[u][c], tf[s][p], acc[c][s]);
+          for (int p = 0; p < Op::NP; ++p) acc[c][s] = El<E>::mma(wf[u][c], tf[s][p], acc[c][s]);
     }
   }
+  out.add(acc);
+}
+
+// ---- the forward in one launch, for few tokens and ranks up to 32: every
+// workgroup forms T of its tile itself (A then is read once for each 512 columns
+// of Y) and adds its columns.  What the second launch costs, some 4 us, is
+// more than those reads as long as they are few.
+struct SmallArgs {
+  const void* X;
+  void* Y;
+  int64_t ldx, ldy;
+  int n, m, tiles;
+  AdSegs seg;
+  const AdEntry* table;
+};
+constexpr int SMALL_WAVES = 8, SMALL_COLS = SMALL_WAVES * 64;
+
+template <typename E, int RT, bool VEC>
+__global__ __launch_bounds__(64 * SMALL_WAVES) void adapter_small_kernel(const SmallArgs a) {
+  using Op = Operands<E, RT>;
+  constexpr int EL = El<E>::EL, KF = El<E>::KF, NK = Op::NK, NC = 4, STEP = 2 * KF, U = 4 / RT;
+  __shared__ __align__(16) float red[SMALL_WAVES][RT * 512];
+  __shared__ __align__(16) float tl[RT * 512];
+  const int64_t w = (int64_t)blockIdx.z * TILES_Y + blockIdx.y;
+  if (w >= a.tiles) return;
+  const AdTile tile = find_tile(a.seg, (int)w);
+  if (tile.rows == 0) return;
+  const AdEntry ad = a.table[tile.adapter];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int jb = blockIdx.x * SMALL_COLS + wave * 64;
+  // what the end needs, on its way while T is formed
+  Columns<E, NC, VEC> out;
+  out.init(a.Y, a.ldy, tile.t0, jb < a.m ? tile.rows : 0, jb, a.m, lane);
+  uint4 wf[NK][NC];
+  {
+    const E* W = static_cast<const E*>(ad.B);
+#pragma unroll
+    for (int u = 0; u < NK; ++u)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        int j = jb + out.col(c, l16);
+        j = j < a.m ? j : a.m - 1;
+        wf[u][c] = load_frag<E, VEC>(W + (int64_t)j * ad.r, u * KF + Op::rank0(g), ad.r, W + (int64_t)a.m * ad.r);
+      }
+  }
+  const E* A = static_cast<const E*>(ad.A);
+  const E* aend = A + (int64_t)ad.r * a.n;
+  const E* x[2];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    if (16 * s + l16 >= in.rows) continue;
-#pragma unroll
-    for (int h = 0; h < NH; ++h) {
-      E* o = y[s] + h * 4 * EL;
-      const int n = left - h * 4 * EL;
-      float v[EL];
-#pragma unroll
-      for (int e = 0; e < EL; ++e) v[e] = acc[h * CP + (e >> 2)][s][e & 3];
-      if (VECY) {
-        if (n > 0) gst16(o, add_frag<E>(yv[s][h], v));
-      } else if (n >= EL) {
-        gst16_u(o, add_frag<E>(gld16_u(o), v));
-      } else {
-#pragma unroll
-        for (int e = 0; e < EL; ++e)
-          if (e < n) {
-            if constexpr (BF) o[e] = f32_to_bits(bits_to_f32(o[e]) + v[e]);
-            else o[e] += v[e];
-          }
-      }
-    }
+    const int t = 16 * s + l16;
+    x[s] = static_cast<const E*>(a.X) + (int64_t)(tile.t0 + (t < tile.rows ? t : 0)) * a.ldx;
   }
+  const E* xend = static_cast<const E*>(a.X) + (int64_t)(a.seg.N - 1) * a.ldx + a.n;
+  const int halves = tile.rows > 16 ? 2 : 1;
+  f32x4 sum[RT][2];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) sum[i][0] = sum[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = wave * STEP; k0 < a.n; k0 += SMALL_WAVES * STEP * U) {
+    uint4 xf[U][2][2], af[U][RT][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = k0 + u * SMALL_WAVES * STEP + h * KF + g * EL;
+        xf[u][0][h] = load_frag<E, VEC>(x[0], k, a.n, xend);
+        xf[u][1][h] = make_uint4(0, 0, 0, 0);
+        if (halves == 2) xf[u][1][h] = load_frag<E, VEC>(x[1], k, a.n, xend);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const int rank = 16 * i + l16;
+          af[u][i][h] = load_frag<E, VEC>(A + (int64_t)(rank < ad.r ? rank : 0) * a.n, k, a.n, aend);
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) sum[i][s] = El<E>::mma(af[u][i][h], xf[u][s][h], sum[i][s]);
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) *reinterpret_cast<f32x4*>(&red[wave][i * 512 + s * 256 + lane * 4]) = sum[i][s];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < SMALL_WAVES; ++q) v += red[q][i * 512 + tid];
+    const int rank = 16 * i + 4 * ((tid >> 6) & 3) + (tid & 3), s = tid >> 8, c = (tid >> 2) & 15;
+    v = rank < ad.r && 16 * s + c < tile.rows ? v * ad.scale : 0.f;
+    const int kk = rank / KF, gg = rank % KF / EL, e = rank % EL, lanes = Op::PACK ? 32 : 64;
+    tl[((kk * 2 + s) * lanes + gg * 16 + c) * EL + e] = v;
+  }
+  __syncthreads();
+  f32x4 acc[NC][2];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) acc[c][0] = acc[c][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int kk = 0; kk < NK; ++kk) {
+    uint4 tf[2][Op::NP];
+    Op::load(tl, kk, lane, tf);
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int p = 0; p < Op::NP; ++p) acc[c][s] = El<E>::mma(wf[kk][c], tf[s][p], acc[c][s]);
+  }
+  out.add(acc);
 }
 
 // ---- outer products: part[slot][rank][col] = sum over a run's tokens of T[rank][t] X[t][col]
@@ -1029,12 +1172,47 @@ void launch_expand(ExpandArgs a, const AdPlan& p, bool vecw, hipStream_t s) {
   }
 }
 
+// Whether the forward goes in one launch: each workgroup then reads its
+// tile of x and all of A, so these have to be small, and the workgroups few.
+// Measured with m, n in {2048, 5632, 4096, 11008, 520, 600}, ranks 8 to 32, 1 to 2048 tokens:
+// where the rule holds one launch takes 8.5 to 12.3 us against 11 to 14.2 us,
+// just outside it 12 to 15 us against 11 us.
+bool small_forward(const poetx_adapters* set, const AdPlan& p, int64_t N, int32_t nseg) {
+  if (p.rpmax > 32) return false;
+  const int64_t tokens = (N + nseg - 1) / nseg < AD_T ? (N + nseg - 1) / nseg : AD_T;   // of a tile, on average
+  const int64_t reads = (p.rpmax + tokens) * set->n * (set->dtype == POETX_F32 ? 4 : 2);
+  const int64_t groups = p.tiles * ((set->m + SMALL_COLS - 1) / SMALL_COLS);
+  return reads <= 200 * 1024 && (groups <= 304 || groups * reads <= 16 << 20);
+}
+
+template <typename E>
+void launch_small(const poetx_adapters* set, const AdSegs& seg, const void* X, int64_t ldx, void* Y, int64_t ldy,
+                  const AdPlan& p, hipStream_t s) {
+  const size_t es = sizeof(E);
+  SmallArgs a{X, Y, ldx, ldy, (int)set->n, (int)set->m, (int)p.tiles, seg, static_cast<const AdEntry*>(set->table)};
+  const bool vec = al16(X) && ldx * es % 16 == 0 && set->n * es % 16 == 0 && al16(Y) && ldy * es % 16 == 0 &&
+                   set->m * es % 16 == 0 && set->layout == (LAY_A16 | LAY_B16);
+  const dim3 grid = tile_grid((set->m + SMALL_COLS - 1) / SMALL_COLS, p.tiles), block(64 * SMALL_WAVES);
+  if (p.rpmax == 16) {
+    if (vec) hipLaunchKernelGGL((adapter_small_kernel<E, 1, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((adapter_small_kernel<E, 1, false>), grid, block, 0, s, a);
+  } else {
+    if (vec) hipLaunchKernelGGL((adapter_small_kernel<E, 2, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((adapter_small_kernel<E, 2, false>), grid, block, 0, s, a);
+  }
+}
+
 template <typename E>
 int forward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, int64_t ldx, void* Y, int64_t ldy,
                  const AdPlan& p, hipStream_t s) {
   const size_t es = sizeof(E);
   const AdEntry* table = static_cast<const AdEntry*>(set->table);
   const double flops = 2.0 * seg.N * set->max_rank;
+  if (small_forward(set, p, seg.N, seg.nseg)) {
+    HostTimer tm(s, "adapter_small", flops * (set->m + set->n), (double)seg.N * (set->n + 2 * set->m) * es);
+    launch_small<E>(set, seg, X, ldx, Y, ldy, p, s);
+    return host_check_launch("adapters forward");
+  }
   {
     HostTimer tm(s, "adapter_shrink", flops * set->n, (double)seg.N * set->n * es);
     ShrinkArgs a{};
