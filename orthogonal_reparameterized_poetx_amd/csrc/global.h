@@ -16,6 +16,12 @@ __device__ __forceinline__ T gld(const T* p) { return *(const POETX_GLOBAL T*)p;
 template <typename T>
 __device__ __forceinline__ void gst(T* p, T v) { *(POETX_GLOBAL T*)p = v; }
 
+// past the caches
+template <typename T>
+__device__ __forceinline__ T gld_nt(const void* p) { return __builtin_nontemporal_load((const POETX_GLOBAL T*)p); }
+template <typename T>
+__device__ __forceinline__ void gst_nt(void* p, T v) { __builtin_nontemporal_store(v, (POETX_GLOBAL T*)p); }
+
 typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));

@@ -19,11 +19,8 @@ namespace poetx {
 
 constexpr int OPT_BLOCK = 256;     // values that share an exponent byte: one wave, four values a lane
 constexpr int OPT_WAVES = 4;
-// blocks a wave has in flight: four; one for sets of up to OPT_FEW blocks, whose
-// chunks would leave most compute units without work (157 blocks: 10.5 us with four)
-constexpr int OPT_UNROLL = 4;
-constexpr int64_t OPT_FEW = 16 * 1024;
-static int chunk_blocks(int64_t blocks) { return OPT_WAVES * (blocks <= OPT_FEW ? 1 : OPT_UNROLL); }
+constexpr int CHUNK_BLOCKS = OPT_WAVES;
+constexpr int64_t OPT_FEW = 16 * 1024;   // blocks of a small set
 
 struct OptChunk {
   void* p;           // at the chunk's first value
@@ -106,16 +103,18 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
 
 struct F4 { float x[4]; };
 
-// four values from `at` on; those at or past `left` read as zero
+// four values from `at` on; those at or past `left` read as zero.  Reads and
+// writes of a step go past the caches (nontemporal): nothing of it is met again
+// before the next step
 __device__ __forceinline__ F4 load4(const void* base, int64_t at, int left, bool bf, bool vec) {
   F4 r;
   if (vec && left >= 4) {
     if (bf) {
-      const u32x2 w = *(const POETX_GLOBAL u32x2*)(static_cast<const uint16_t*>(base) + at);
+      const u32x2 w = gld_nt<u32x2>(static_cast<const uint16_t*>(base) + at);
       r.x[0] = __uint_as_float(w.x << 16); r.x[1] = __uint_as_float(w.x & 0xffff0000u);
       r.x[2] = __uint_as_float(w.y << 16); r.x[3] = __uint_as_float(w.y & 0xffff0000u);
     } else {
-      const f32x4 w = *(const POETX_GLOBAL f32x4*)(static_cast<const float*>(base) + at);
+      const f32x4 w = gld_nt<f32x4>(static_cast<const float*>(base) + at);
       r.x[0] = w[0]; r.x[1] = w[1]; r.x[2] = w[2]; r.x[3] = w[3];
     }
     return r;
@@ -129,7 +128,7 @@ __device__ __forceinline__ F4 load4(const void* base, int64_t at, int left, bool
 
 __device__ __forceinline__ void store4_bf16(uint16_t* base, int64_t at, int left, bool vec, const uint16_t h[4]) {
   if (vec && left >= 4) {
-    *(POETX_GLOBAL u32x2*)(base + at) = u32x2{pack2(h[0], h[1]), pack2(h[2], h[3])};
+    gst_nt(base + at, u32x2{pack2(h[0], h[1]), pack2(h[2], h[3])});
     return;
   }
 #pragma unroll
@@ -146,125 +145,122 @@ struct StepArgs {
   uint32_t step;
 };
 
+// A workgroup takes a chunk, each wave one block: small workgroups in the order
+// of the memory.  With four blocks a wave, all loads ahead, 135.6 M values with
+// 8-bit moments took 431 us, with two 418 us, with one 404 us; past the caches and
+// with the hardware's reciprocal and root (one ulp each, on an update that is
+// some 1e-3 of p) 353 us, 6.1 TB/s of the 16 bytes a value.
 // The moments are formed with separate roundings (no contraction): the codes
 // of the 8-bit state then follow from the formula alone.
-template <bool Q8, int U>
+template <bool Q8>
 __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
 #pragma clang fp contract(off)
   const OptChunk ch = a.chunks[blockIdx.x];
   const float coef = a.coef ? *a.coef : 1.f;
-  if (!(fabsf(coef) < INFINITY)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int at = wave * OPT_BLOCK + lane * 4;
+  const bool in = wave * OPT_BLOCK < ch.left;   // (a wave without a block reads the chunk's first)
   const float lr = a.lr * ch.lr_mul;
   const bool pbf = ch.flags & OPT_PBF, gbf = ch.flags & OPT_GBF, vec = ch.flags & OPT_VEC;
-  F4 p[U], g[U], m[U], v[U];
-  uint32_t mc[U], vc[U];
-  int Em[U], Ev[U];
-  int left[U];   // values of the tensor from this lane's first on
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const int blk = wave * U + i, at = blk * OPT_BLOCK + lane * 4, l = ch.left - at;
-    left[i] = l < 0 ? 0 : l > 4 ? 4 : l;
-    if (blk * OPT_BLOCK < ch.left) {
-      p[i] = load4(ch.p, at, left[i], pbf, vec);
-      g[i] = load4(ch.g, at, left[i], gbf, vec);
-      const int64_t s = (ch.block + blk) * OPT_BLOCK + lane * 4;
-      if (Q8) {
-        Em[i] = a.me[ch.block + blk];
-        Ev[i] = a.ve[ch.block + blk];
-        mc[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s);
-        vc[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s);
-      } else {
-        const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.m) + s);
-        const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + s);
-        m[i].x[0] = x.x; m[i].x[1] = x.y; m[i].x[2] = x.z; m[i].x[3] = x.w;
-        v[i].x[0] = y.x; v[i].x[1] = y.y; v[i].x[2] = y.z; v[i].x[3] = y.w;
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < U; ++i) {
-    const int blk = wave * U + i, at = blk * OPT_BLOCK + lane * 4;
-    if (blk * OPT_BLOCK >= ch.left) continue;
-    const int64_t sb = ch.block + blk, s = sb * OPT_BLOCK + lane * 4;
-    if (Q8) {
-      const int em = exp_of(Em[i]), ev = exp_of(Ev[i]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        m[i].x[j] = em == 255 ? NAN : decode8<true>(mc[i] >> (8 * j) & 255u, em);
-        v[i].x[j] = ev == 255 ? NAN : decode8<false>(vc[i] >> (8 * j) & 255u, ev);
-      }
-    }
-    const uint32_t h0 = (uint32_t)s * kAlphaPos + a.step * kAlphaStep;
-    uint16_t pb[4], cb[4];
+  const int l = ch.left - at, left = l < 0 ? 0 : l > 4 ? 4 : l;   // values of the tensor from this lane's first on
+  const int64_t sb = ch.block + (in ? wave : 0), s = sb * OPT_BLOCK + lane * 4;
+  // every load before the first use of one
+  F4 p = load4(ch.p, at, left, pbf, vec);
+  const F4 g = load4(ch.g, at, left, gbf, vec);
+  F4 m, v;
+  uint32_t mc, vc;
+  int em, ev;
+  if (Q8) {
+    em = a.me[sb];
+    ev = a.ve[sb];
+    mc = gld(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s));
+    vc = gld(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s));
+  } else {
+    const f32x4 x = gld_nt<f32x4>(static_cast<const float*>(a.m) + s);
+    const f32x4 y = gld_nt<f32x4>(static_cast<const float*>(a.v) + s);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float gj = g[i].x[j] * coef;
-      float mj = m[i].x[j] * a.b1 + gj * a.ob1;
-      float vj = v[i].x[j] * a.b2 + gj * gj * a.ob2;
-      if (j >= left[i]) mj = vj = 0.f;   // padding
-      m[i].x[j] = mj;
-      v[i].x[j] = vj;
-      const float up = (mj * a.ibc1) / (sqrtf(vj * a.ibc2) + a.eps);
-      const float q = p[i].x[j] - lr * (ch.decay * p[i].x[j] + up);
-      p[i].x[j] = q;
-      // the carry of the dither must not turn infinity or NaN into another value
-      const uint32_t qb = __float_as_uint(q);
-      const uint32_t d = (h0 + (uint32_t)j * kAlphaPos) >> 16;
-      pb[j] = (uint16_t)((qb & 0x7f800000u) == 0x7f800000u ? f32_to_bits(q) : (qb + d) >> 16);
-      cb[j] = f32_to_bits(q);
+      m.x[j] = x[j];
+      v.x[j] = y[j];
     }
-    if (pbf) {
-      store4_bf16(static_cast<uint16_t*>(ch.p), at, left[i], vec, pb);
+  }
+  if (!in || !(fabsf(coef) < INFINITY)) return;
+  if (Q8) {
+    em = exp_of(em);
+    ev = exp_of(ev);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      m.x[j] = em == 255 ? NAN : decode8<true>(mc >> (8 * j) & 255u, em);
+      v.x[j] = ev == 255 ? NAN : decode8<false>(vc >> (8 * j) & 255u, ev);
+    }
+  }
+  const uint32_t h0 = (uint32_t)s * kAlphaPos + a.step * kAlphaStep;
+  uint16_t pb[4], cb[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float gj = g.x[j] * coef;
+    float mj = m.x[j] * a.b1 + gj * a.ob1;
+    float vj = v.x[j] * a.b2 + gj * gj * a.ob2;
+    if (j >= left) mj = vj = 0.f;   // padding
+    m.x[j] = mj;
+    v.x[j] = vj;
+    const float up = (mj * a.ibc1) * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(vj * a.ibc2) + a.eps);
+    const float q = p.x[j] - lr * (ch.decay * p.x[j] + up);
+    p.x[j] = q;
+    // the carry of the dither must not turn infinity or NaN into another value
+    const uint32_t qb = __float_as_uint(q);
+    const uint32_t d = (h0 + (uint32_t)j * kAlphaPos) >> 16;
+    pb[j] = (uint16_t)((qb & 0x7f800000u) == 0x7f800000u ? f32_to_bits(q) : (qb + d) >> 16);
+    cb[j] = f32_to_bits(q);
+  }
+  if (pbf) {
+    store4_bf16(static_cast<uint16_t*>(ch.p), at, left, vec, pb);
+  } else {
+    float* dst = static_cast<float*>(ch.p) + at;
+    if (vec && left == 4) {
+      gst_nt(dst, f32x4{p.x[0], p.x[1], p.x[2], p.x[3]});
     } else {
-      float* dst = static_cast<float*>(ch.p) + at;
-      if (vec && left[i] == 4) {
-        *(POETX_GLOBAL f32x4*)dst = f32x4{p[i].x[0], p[i].x[1], p[i].x[2], p[i].x[3]};
-      } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < left[i]) gst(dst + j, p[i].x[j]);
-      }
-      if (ch.copy) store4_bf16(ch.copy, at, left[i], vec, cb);
+      for (int j = 0; j < 4; ++j)
+        if (j < left) gst(dst + j, p.x[j]);
     }
-    if (Q8) {
-      uint32_t xm = 0, xv = 0;
+    if (ch.copy) store4_bf16(ch.copy, at, left, vec, cb);
+  }
+  if (Q8) {
+    uint32_t xm = 0, xv = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t bm = __float_as_uint(m[i].x[j]) & 0x7fffffffu, bv = __float_as_uint(v[i].x[j]) & 0x7fffffffu;
-        xm = xm > bm ? xm : bm;
-        xv = xv > bv ? xv : bv;
-      }
-      const int em = block_exp(wave_max(xm)), ev = block_exp(wave_max(xv));
-      uint32_t om = 0, ov = 0;
-      if (em != 255) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          om |= encode8<true>(m[i].x[j], (h0 + (uint32_t)j * kAlphaPos) >> 12, em) << (8 * j);
-      }
-      if (ev != 255) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          ov |= encode8<false>(v[i].x[j], (h0 + (uint32_t)j * kAlphaPos) >> 5 & 0xFFFFFu, ev) << (8 * j);
-      }
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s) = om;
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s) = ov;
-      if (lane == 0) {
-        a.me[sb] = (uint8_t)em;
-        a.ve[sb] = (uint8_t)ev;
-      }
-    } else {
-      *reinterpret_cast<float4*>(static_cast<float*>(a.m) + s) =
-          make_float4(m[i].x[0], m[i].x[1], m[i].x[2], m[i].x[3]);
-      *reinterpret_cast<float4*>(static_cast<float*>(a.v) + s) =
-          make_float4(v[i].x[0], v[i].x[1], v[i].x[2], v[i].x[3]);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t bm = __float_as_uint(m.x[j]) & 0x7fffffffu, bv = __float_as_uint(v.x[j]) & 0x7fffffffu;
+      xm = xm > bm ? xm : bm;
+      xv = xv > bv ? xv : bv;
     }
+    em = block_exp(wave_max(xm));
+    ev = block_exp(wave_max(xv));
+    uint32_t om = 0, ov = 0;
+    if (em != 255) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) om |= encode8<true>(m.x[j], (h0 + (uint32_t)j * kAlphaPos) >> 12, em) << (8 * j);
+    }
+    if (ev != 255) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        ov |= encode8<false>(v.x[j], (h0 + (uint32_t)j * kAlphaPos) >> 5 & 0xFFFFFu, ev) << (8 * j);
+    }
+    gst(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s), om);
+    gst(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s), ov);
+    if (lane == 0) {
+      a.me[sb] = (uint8_t)em;
+      a.ve[sb] = (uint8_t)ev;
+    }
+  } else {
+    gst_nt(static_cast<float*>(a.m) + s, f32x4{m.x[0], m.x[1], m.x[2], m.x[3]});
+    gst_nt(static_cast<float*>(a.v) + s, f32x4{v.x[0], v.x[1], v.x[2], v.x[3]});
   }
 }
 
 // Squares are exact in fp64 and cannot overflow; their sums keep far more
 // bits than the fp32 result, whatever the count.  The four waves of team t (of
-// NORM_TEAMS a workgroup) sum the chunks t, t + teams, ..., two at a time; the
+// NORM_TEAMS a workgroup) sum every teams-th group of K chunks; the
 // last workgroup to arrive adds the partial sums in index order, so the
 // result does not depend on the order of arrival.  Arrivals wait for one
 // another, some 20 ns each, so there is one workgroup for each compute unit:
@@ -272,7 +268,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
 // 2048 of four waves 153 us.  fp64 sums cost nothing: with fp32 sums as long.
 constexpr int NORM_TEAMS = 2, NORM_WAVES = NORM_TEAMS * OPT_WAVES;
 
-template <int U>
+template <int K>
 __global__ __launch_bounds__(64 * NORM_WAVES) void grad_norm_kernel(OptHead* head, const OptChunk* chunks, int64_t nchunks,
                                                         float max_norm, double* part, float* out) {
   __shared__ double red[NORM_WAVES];
@@ -280,26 +276,20 @@ __global__ __launch_bounds__(64 * NORM_WAVES) void grad_norm_kernel(OptHead* hea
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % OPT_WAVES;
   const int64_t teams = (int64_t)gridDim.x * NORM_TEAMS;
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
-  for (int64_t c = blockIdx.x * NORM_TEAMS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 8); c < nchunks; c += 2 * teams) {
-    F4 g[2][U];
+  for (int64_t c = K * (int64_t)(blockIdx.x * NORM_TEAMS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 8)); c < nchunks;
+       c += K * teams) {
+    F4 g[K];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int64_t ck = c + k * teams;
+    for (int k = 0; k < K; ++k) {
+      const int64_t ck = c + k;
       const OptChunk* ch = chunks + (ck < nchunks ? ck : c);
-      const void* src = ch->g;
-      const int n = ck < nchunks ? ch->left : 0, flags = ch->flags;
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int at = (wave * U + i) * OPT_BLOCK + lane * 4, l = n - at;
-        g[k][i] = load4(src, at, l < 0 ? 0 : l > 4 ? 4 : l, flags & OPT_GBF, flags & OPT_VEC);
-      }
+      const int at = wave * OPT_BLOCK + lane * 4, l = (ck < nchunks ? ch->left : 0) - at;
+      g[k] = load4(ch->g, at, l < 0 ? 0 : l > 4 ? 4 : l, ch->flags & OPT_GBF, ch->flags & OPT_VEC);
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = fma((double)g[k][i].x[j], (double)g[k][i].x[j], acc[j]);
+      for (int j = 0; j < 4; ++j) acc[j] = fma((double)g[k].x[j], (double)g[k].x[j], acc[j]);
   }
   double sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
   auto block_sum = [&](double x) {
@@ -398,11 +388,11 @@ int plan_params(const poetx_param* params, int32_t count, int64_t* blocks, int64
     if (rc) return rc;
     if (params[i].count > (int64_t(1) << 37) - *values)
       return host_fail(POETX_ESHAPE, "more than 2^37 values in one set");
-    *blocks += (params[i].count + OPT_BLOCK - 1) / OPT_BLOCK;
+    const int64_t b = (params[i].count + OPT_BLOCK - 1) / OPT_BLOCK;
+    *blocks += b;
+    *chunks += (b + CHUNK_BLOCKS - 1) / CHUNK_BLOCKS;
     *values += params[i].count;
   }
-  const int per = chunk_blocks(*blocks);
-  for (int32_t i = 0; i < count; ++i) *chunks += ((params[i].count + OPT_BLOCK - 1) / OPT_BLOCK + per - 1) / per;
   return POETX_OK;
 }
 
@@ -454,7 +444,7 @@ int poetx_param_table(const poetx_param* params, int32_t count, void* host_table
   if (bytes < need) return host_fail(POETX_EWORKSPACE, "table has %zu bytes, needs %zu", bytes, need);
   memset(host_table, 0, sizeof(OptHead));
   OptChunk* c = reinterpret_cast<OptChunk*>(static_cast<char*>(host_table) + sizeof(OptHead));
-  const int64_t span = (int64_t)chunk_blocks(blocks) * OPT_BLOCK;
+  const int64_t span = (int64_t)CHUNK_BLOCKS * OPT_BLOCK;
   int64_t block = 0;
   uint32_t norm_only = 0;
   for (int32_t i = 0; i < count; ++i) {
@@ -495,10 +485,10 @@ int poetx_grad_norm(const poetx_param_set* set, float max_norm, float* out, void
     OptHead* head = static_cast<OptHead*>(const_cast<void*>(set->table));
     double* part = static_cast<double*>(ws);
     if (set->blocks <= OPT_FEW)
-      hipLaunchKernelGGL(grad_norm_kernel<1>, dim3((unsigned)grid), dim3(64 * NORM_WAVES), 0, s, head, chunks_of(set), set->chunks,
-                         max_norm, part, out);
+      hipLaunchKernelGGL(grad_norm_kernel<2>, dim3((unsigned)grid), dim3(64 * NORM_WAVES), 0, s, head, chunks_of(set),
+                         set->chunks, max_norm, part, out);
     else
-      hipLaunchKernelGGL(grad_norm_kernel<OPT_UNROLL>, dim3((unsigned)grid), dim3(64 * NORM_WAVES), 0, s, head, chunks_of(set),
+      hipLaunchKernelGGL(grad_norm_kernel<8>, dim3((unsigned)grid), dim3(64 * NORM_WAVES), 0, s, head, chunks_of(set),
                          set->chunks, max_norm, part, out);
   }
   return host_check_launch("gradient norm");
@@ -531,13 +521,8 @@ int poetx_adamw_step(const poetx_param_set* set, const poetx_adamw_state* state,
     const bool q8 = state->kind == POETX_STATE_8BIT;
     HostTimer tm(s, "adamw", 0.0, (q8 ? 16.0 : 28.0) * set->values);
     const dim3 grid((unsigned)set->chunks), block(256);
-    if (set->blocks <= OPT_FEW) {
-      if (q8) hipLaunchKernelGGL((adamw_kernel<true, 1>), grid, block, 0, s, a);
-      else hipLaunchKernelGGL((adamw_kernel<false, 1>), grid, block, 0, s, a);
-    } else {
-      if (q8) hipLaunchKernelGGL((adamw_kernel<true, OPT_UNROLL>), grid, block, 0, s, a);
-      else hipLaunchKernelGGL((adamw_kernel<false, OPT_UNROLL>), grid, block, 0, s, a);
-    }
+    if (q8) hipLaunchKernelGGL(adamw_kernel<true>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(adamw_kernel<false>, grid, block, 0, s, a);
   }
   return host_check_launch("adamw");
 }
