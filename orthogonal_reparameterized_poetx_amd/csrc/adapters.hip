@@ -102,11 +102,14 @@ template <> struct El<float> {
 // elements k .. k + EL of a row of `width`, zeros past its end.  VEC: rows of
 // whole 16-byte pieces.  Otherwise the piece may start at any element (global
 // loads of 16 bytes need no alignment beyond the element's) and is cut at the row's
-// end; `end` is the end of the matrix, past which nothing is read.
-template <typename E, bool VEC>
+// end; `end` is the end of the matrix, past which nothing is read.  NT: past the caches.
+template <typename E, bool VEC, bool NT = false>
 __device__ __forceinline__ uint4 load_frag(const E* row, int k, int width, const E* end) {
   constexpr int EL = El<E>::EL;
-  if (VEC) return k < width ? gld16(row + k) : make_uint4(0, 0, 0, 0);
+  if (VEC)
+    return k >= width ? make_uint4(0, 0, 0, 0)
+           : NT       ? __builtin_bit_cast(uint4, gld_nt<u32x4>(row + k))
+                      : gld16(row + k);
   const int left = width - k;
   uint4 v = make_uint4(0, 0, 0, 0);
   if (left <= 0) return v;
@@ -263,7 +266,7 @@ constexpr int shrink_lds(int rt, int es) {
   return most > TURN_LDS ? most : TURN_LDS;
 }
 
-template <typename E, int RT, bool VEC, bool USEB>
+template <typename E, int RT, bool VEC, bool NT, bool USEB>
 __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob& J, const AdTile& tile, int w,
                                             int group, int part, char* lds) {
   constexpr int EL = El<E>::EL, KF = El<E>::KF, ES = sizeof(E), THREADS = 64 * SHRINK_WAVES;
@@ -302,7 +305,7 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const int c = i * THREADS + tid, row = c / PR, k = k0 + c % PR * EL;
-      xr[i] = load_frag<E, VEC>(X + (int64_t)(row < tile.rows ? row : 0) * J.ldx, k, J.width, xend);
+      xr[i] = load_frag<E, VEC, NT>(X + (int64_t)(row < tile.rows ? row : 0) * J.ldx, k, J.width, xend);
     }
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
@@ -398,7 +401,7 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
 
 constexpr int TILES_Y = 32768;   // tiles along the grid's second dimension
 
-template <typename E, int RT, bool VEC>
+template <typename E, int RT, bool VEC, bool NT>
 __global__ __launch_bounds__(64 * SHRINK_WAVES) void adapter_shrink_kernel(const ShrinkArgs a) {
   __shared__ __align__(16) char lds[shrink_lds(RT, sizeof(E))];
   const int64_t w = (int64_t)blockIdx.z * TILES_Y + blockIdx.y;
@@ -426,8 +429,8 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void adapter_shrink_kernel(const
   const ShrinkJob& J = a.job[x >= n0];
   if (x >= n0) x -= n0;
   const int part = x / a.groups, group = x % a.groups;
-  if (J.useB) shrink_body<E, RT, VEC, true>(a, J, tile, (int)w, group, part, lds);
-  else shrink_body<E, RT, VEC, false>(a, J, tile, (int)w, group, part, lds);
+  if (J.useB) shrink_body<E, RT, VEC, NT, true>(a, J, tile, (int)w, group, part, lds);
+  else shrink_body<E, RT, VEC, NT, false>(a, J, tile, (int)w, group, part, lds);
 }
 
 // ---- expand: Y[t][j] += sum_k T[k][t] W[j][k], W = each adapter's B, or (dx) At
@@ -847,7 +850,7 @@ struct OuterArgs {
 // slot); a second kernel adds an adapter's slots in order.  A slot is written
 // and read as fp32, rank x (n + m): with a run for each wave those bytes
 // outweighed the activations (the same case: 32.8 us).
-template <typename E, bool VEC>
+template <typename E, bool VEC, bool NT>
 __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
   constexpr int EL = El<E>::EL, COLS = 16 * EL, LD = COLS + 4;
   constexpr bool BF = EL == 8;
@@ -870,7 +873,7 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
     for (int i = 0; i < 8; ++i) {
       const int t = BF ? 8 * g + i : 4 * i + g;
       // past the tile's end T is zero, but 0 x NaN is not
-      x[i] = t < en.y ? load_frag<E, VEC>(X + (int64_t)t * J.ldx, col, J.width, xend) : make_uint4(0, 0, 0, 0);
+      x[i] = t < en.y ? load_frag<E, VEC, NT>(X + (int64_t)t * J.ldx, col, J.width, xend) : make_uint4(0, 0, 0, 0);
     }
   };
   while (e0 < e1) {
@@ -1077,14 +1080,17 @@ AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd,
   const bool f32 = s->dtype == POETX_F32;
   p.tiles = N / AD_T + nseg;
   p.rpmax = pad_rank(s->max_rank, s->max_rank);
-  // the shrink's parts: about 1024 workgroups, of 512 columns at least; where
-  // these are too few still, the ranks are shared out as well (x is then read again)
+  // the shrink's parts: 1024 columns; with very many workgroups 2048, with few
+  // 512; where these are too few still, the ranks are shared out as well
+  // (x is then read again).  Measured with parts of 512, 1024, 1536, 2048, 2560,
+  // 3072 columns: 4099 x 5632 (rank 32) 33.2, 28.8, 27.4, 34.2, 34.9, 33.5 us, 8192 x 2048
+  // -> 5632 58.8, 55.4, 58.0, 57.6, 57.8, 57.7 us, backward of 2001 x 2048 (rank 64) 49.2,
+  // 45.5, 50.3, 50.0, 49.7, 49.3 us, of 8192 x 4096 -> 11008 170, 154, 151, 153, 152, 153 us.
   const int rt_all = p.rpmax / 16;
   p.rt = rt_all < 4 ? ceil_rt(rt_all) : 4;
   auto groups = [&](int rt) { return (rt_all + rt - 1) / rt; };
-  const int64_t widths = s->n + (bwd ? s->m : 0);
-  int64_t pw = (p.tiles * groups(p.rt) * widths / 1024 + 511) / 512 * 512;
-  p.pw = (int)(pw < 512 ? 512 : pw > 32768 ? 32768 : pw);
+  const int64_t parts1k = p.tiles * (s->n + (bwd ? s->m : 0)) / 1024;
+  p.pw = parts1k > 2048 ? 2048 : parts1k < 128 ? 512 : 1024;
   p.parts[0] = (int)((s->n + p.pw - 1) / p.pw);
   p.parts[1] = bwd ? (int)((s->m + p.pw - 1) / p.pw) : 0;
   while (p.rt > 1 && p.tiles * groups(p.rt) * (p.parts[0] + p.parts[1]) < 512) p.rt /= 2;
@@ -1121,6 +1127,16 @@ AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd,
   return p;
 }
 
+// Activations of this many bytes are read past the caches: they would not
+// survive beside the rest in the 256 MiB that the memory side holds.  Measured:
+// 8192 x 2048 -> 5632 (126 MB) 53.2 us instead of 55.4, backward of 8192 x 4096 ->
+// 11008 (314 MB) 139.5 us instead of 152.6; 4099 x 5632 -> 2048 (63 MB) 30.4 us instead of 28.8,
+// backward of 2001 x 2048 (25 MB) 52.8 us instead of 50.0.
+constexpr int64_t STREAM_BYTES = 96ll << 20;
+bool streams(const poetx_adapters* s, int64_t N) {
+  return N * (s->n + s->m) * (s->dtype == POETX_F32 ? 4 : 2) > STREAM_BYTES;
+}
+
 // x workgroups of each of `count` tiles (or more)
 dim3 tile_grid(int64_t x, int64_t count) {
   return dim3((unsigned)x, (unsigned)(count < TILES_Y ? count : TILES_Y), (unsigned)((count + TILES_Y - 1) / TILES_Y));
@@ -1131,17 +1147,19 @@ AdSegs segs_of(const poetx_adapters* s, const int32_t* start, const int32_t* whi
 }
 
 template <typename E>
-void launch_shrink(ShrinkArgs a, const AdPlan& p, int64_t extra, bool vec, hipStream_t s) {
+void launch_shrink(ShrinkArgs a, const AdPlan& p, int64_t extra, bool vec, bool nt, hipStream_t s) {
   a.rpmax = p.rpmax;
   a.tiles = (int)p.tiles;
   a.info = p.info;
   a.pw = p.pw;
   a.groups = p.rgroups;
   const dim3 grid = tile_grid((p.parts[0] + p.parts[1]) * p.rgroups, p.tiles + extra);
+  const dim3 block(64 * SHRINK_WAVES);
 #define POETX_RT(R) \
   case R: \
-    if (vec) hipLaunchKernelGGL((adapter_shrink_kernel<E, R, true>), grid, dim3(64 * SHRINK_WAVES), 0, s, a); \
-    else hipLaunchKernelGGL((adapter_shrink_kernel<E, R, false>), grid, dim3(64 * SHRINK_WAVES), 0, s, a); \
+    if (vec && nt) hipLaunchKernelGGL((adapter_shrink_kernel<E, R, true, true>), grid, block, 0, s, a); \
+    else if (vec) hipLaunchKernelGGL((adapter_shrink_kernel<E, R, true, false>), grid, block, 0, s, a); \
+    else hipLaunchKernelGGL((adapter_shrink_kernel<E, R, false, false>), grid, block, 0, s, a); \
     break;
   switch (p.rt) { POETX_RT(1) POETX_RT(2) POETX_RT(4) }
 #undef POETX_RT
@@ -1220,7 +1238,7 @@ int forward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, in
     a.seg = seg;
     a.table = table;
     const bool vec = al16(X) && ldx * es % 16 == 0 && set->n * es % 16 == 0 && (set->layout & LAY_A16);
-    launch_shrink<E>(a, p, 0, vec, s);
+    launch_shrink<E>(a, p, 0, vec, streams(set, seg.N), s);
   }
   {
     HostTimer tm(s, "adapter_expand", flops * set->m, 2.0 * seg.N * set->m * es);
@@ -1240,6 +1258,7 @@ int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, i
   const double flops = 2.0 * seg.N * set->max_rank;
   const bool xvec = al16(X) && ldx * es % 16 == 0 && n * es % 16 == 0;
   const bool yvec = al16(dY) && lddy * es % 16 == 0 && m * es % 16 == 0;
+  const bool nt = streams(set, seg.N);
   const ListArgs lists{p.list, p.offs, (int)p.tiles};
   if (p.tiles == 0) {
     hipLaunchKernelGGL(adapter_list_kernel, dim3((unsigned)set->count), dim3(256), 0, s, seg, lists);
@@ -1257,7 +1276,7 @@ int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, i
       while (tw > 8 && (size_t)tw * (set->max_rank + 3) * es > TURN_LDS) tw /= 2;
       a.turn = TurnArgs{dX ? p.At : nullptr, n, (n + tw - 1) / tw, tw};
       launch_shrink<E>(a, p, (int64_t)set->count * (1 + (dX ? a.turn.per : 0)), xvec && yvec && set->layout == (LAY_A16 | LAY_B16),
-                       s);
+                       nt, s);
     }
     {
       HostTimer tm(s, "adapter_expand", flops * n, 2.0 * seg.N * n * es);
@@ -1275,8 +1294,9 @@ int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, i
       a.list = p.list; a.offs = p.offs; a.count = set->count; a.rpmax = p.rpmax; a.run = p.run; a.slabs0 = p.slabs[0];
       a.N = seg.N;
       const dim3 grid((unsigned)(p.slabs[0] + p.slabs[1]), (unsigned)p.runs, (unsigned)(p.rpmax / 16));
-      if (xvec && yvec) hipLaunchKernelGGL((adapter_outer_kernel<E, true>), grid, dim3(256), 0, s, a);
-      else hipLaunchKernelGGL((adapter_outer_kernel<E, false>), grid, dim3(256), 0, s, a);
+      if (xvec && yvec && nt) hipLaunchKernelGGL((adapter_outer_kernel<E, true, true>), grid, dim3(256), 0, s, a);
+      else if (xvec && yvec) hipLaunchKernelGGL((adapter_outer_kernel<E, true, false>), grid, dim3(256), 0, s, a);
+      else hipLaunchKernelGGL((adapter_outer_kernel<E, false, false>), grid, dim3(256), 0, s, a);
     }
   }
   {
