@@ -99,6 +99,12 @@ template <> struct El<float> {
   }
 };
 
+// 16 bytes that lie within a row
+template <bool VEC, bool NT>
+__device__ __forceinline__ uint4 load_whole(const void* p) {
+  return !VEC ? gld16_u(p) : NT ? __builtin_bit_cast(uint4, gld_nt<u32x4>(p)) : gld16(p);
+}
+
 // elements k .. k + EL of a row of `width`, zeros past its end.  VEC: rows of
 // whole 16-byte pieces.  Otherwise the piece may start at any element (global
 // loads of 16 bytes need no alignment beyond the element's) and is cut at the row's
@@ -107,9 +113,7 @@ template <typename E, bool VEC, bool NT = false>
 __device__ __forceinline__ uint4 load_frag(const E* row, int k, int width, const E* end) {
   constexpr int EL = El<E>::EL;
   if (VEC)
-    return k >= width ? make_uint4(0, 0, 0, 0)
-           : NT       ? __builtin_bit_cast(uint4, gld_nt<u32x4>(row + k))
-                      : gld16(row + k);
+    return k < width ? load_whole<true, NT>(row + k) : make_uint4(0, 0, 0, 0);
   const int left = width - k;
   uint4 v = make_uint4(0, 0, 0, 0);
   if (left <= 0) return v;
@@ -302,10 +306,12 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
   for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
   uint4 xr[NX], wr[NW];
   auto load = [&](int k0) {   // the chunk from column k0 on
+    const bool whole = k0 + CW <= J.width;
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const int c = i * THREADS + tid, row = c / PR, k = k0 + c % PR * EL;
-      xr[i] = load_frag<E, VEC, NT>(X + (int64_t)(row < tile.rows ? row : 0) * J.ldx, k, J.width, xend);
+      const E* x = X + (int64_t)(row < tile.rows ? row : 0) * J.ldx;
+      xr[i] = whole ? load_whole<VEC, NT>(x + k) : load_frag<E, VEC, NT>(x, k, J.width, xend);
     }
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
@@ -315,7 +321,8 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
                                             : make_uint4(0, 0, 0, 0);
       } else {
         const int c = i * THREADS + tid, rank = rank0 + c / PR, k = k0 + c % PR * EL;
-        wr[i] = load_frag<E, VEC>(W + (int64_t)(rank < ad.r ? rank : 0) * J.width, k, J.width, wend);
+        const E* r = W + (int64_t)(rank < ad.r ? rank : 0) * J.width;
+        wr[i] = whole ? load_whole<VEC, false>(r + k) : load_frag<E, VEC>(r, k, J.width, wend);
       }
     }
   };
@@ -834,7 +841,7 @@ struct OuterArgs {
   OuterJob job[2];
   const int4* list;
   const int32_t* offs;
-  int count, rpmax, run, slabs0;   // run: list entries of a workgroup; slabs0: slabs of job 0
+  int count, rpmax, run, slabs, slabs0, groups;   // run: list entries of a workgroup; slabs0: slabs of job 0; groups of 16 ranks
   int N;
 };
 
@@ -855,11 +862,15 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
   constexpr int EL = El<E>::EL, COLS = 16 * EL, LD = COLS + 4;
   constexpr bool BF = EL == 8;
   __shared__ __align__(16) float red[4][16 * LD];
-  int bx = blockIdx.x;
+  // the rank groups of eight slabs follow one another, those of a slab eight
+  // workgroups apart: on the same eighth of the chip, whose cache gives them x again
+  const int octet = blockIdx.x / (8 * a.groups), in = blockIdx.x % (8 * a.groups);
+  int bx = octet * 8 + in % 8;
+  const int rank0 = in / 8 * 16;
+  if (bx >= a.slabs) return;
   const int jz = bx >= a.slabs0;
   if (jz) bx -= a.slabs0;
   const OuterJob& J = a.job[jz];
-  const int rank0 = blockIdx.z * 16;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int cb = bx * COLS, col = cb + l16 * EL;
@@ -867,13 +878,16 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
   int e0 = blockIdx.y * a.run, e1 = e0 + a.run;
   if (e1 > total) e1 = total;
   const E* xend = static_cast<const E*>(J.X) + (int64_t)(a.N - 1) * J.ldx + J.width;
+  const bool whole = cb + COLS <= J.width;
   auto load = [&](uint4 (&x)[8], const int4& en) {
     const E* X = static_cast<const E*>(J.X) + (int64_t)en.x * J.ldx;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int t = BF ? 8 * g + i : 4 * i + g;
       // past the tile's end T is zero, but 0 x NaN is not
-      x[i] = t < en.y ? load_frag<E, VEC, NT>(X + (int64_t)t * J.ldx, col, J.width, xend) : make_uint4(0, 0, 0, 0);
+      const E* row = X + (int64_t)t * J.ldx;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (t < en.y) x[i] = whole ? load_whole<VEC, NT>(row + col) : load_frag<E, VEC, NT>(row, col, J.width, xend);
     }
   };
   while (e0 < e1) {
@@ -1292,8 +1306,9 @@ int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, i
       a.job[0] = OuterJob{X, p.U, p.part[0], ldx, n};
       a.job[1] = OuterJob{dY, p.T, p.part[1], lddy, m};
       a.list = p.list; a.offs = p.offs; a.count = set->count; a.rpmax = p.rpmax; a.run = p.run; a.slabs0 = p.slabs[0];
+      a.slabs = p.slabs[0] + p.slabs[1]; a.groups = p.rpmax / 16;
       a.N = seg.N;
-      const dim3 grid((unsigned)(p.slabs[0] + p.slabs[1]), (unsigned)p.runs, (unsigned)(p.rpmax / 16));
+      const dim3 grid((unsigned)((a.slabs + 7) / 8 * 8 * a.groups), (unsigned)p.runs);
       if (xvec && yvec && nt) hipLaunchKernelGGL((adapter_outer_kernel<E, true, true>), grid, dim3(256), 0, s, a);
       else if (xvec && yvec) hipLaunchKernelGGL((adapter_outer_kernel<E, true, false>), grid, dim3(256), 0, s, a);
       else hipLaunchKernelGGL((adapter_outer_kernel<E, false, false>), grid, dim3(256), 0, s, a);
