@@ -21,6 +21,9 @@ class AdapterSet:
     A batch is cut into segments of consecutive tokens: seg_start (int32,
     one more entry than segments) and seg_adapter (int32, an index into the
     set or -1), both on the device.
+
+    Calls run on the current stream.  Those of one object share its
+    workspaces: on several streams at once, use an object for each.
     """
 
     def __init__(self, m, n, A, B, scales, dA=None, dB=None):

@@ -105,35 +105,54 @@ __device__ __forceinline__ uint4 load_whole(const void* p) {
   return !VEC ? gld16_u(p) : NT ? __builtin_bit_cast(uint4, gld_nt<u32x4>(p)) : gld16(p);
 }
 
-// elements k .. k + EL of a row of `width`, zeros past its end.  VEC: rows of
-// whole 16-byte pieces.  Otherwise the piece may start at any element (global
-// loads of 16 bytes need no alignment beyond the element's) and is cut at the row's
-// end; `end` is the end of the matrix, past which nothing is read.  NT: past the caches.
+// Elements k .. k + EL of a row of `width`, zeros past its end.  VEC: rows of
+// whole 16-byte pieces, and the load is all.  Otherwise the piece may start at
+// any element (global loads of 16 bytes need no alignment beyond the element's):
+// load_frag loads what lies before `end`, the end of the matrix; rest_frag then
+// loads the matrix's last elements one by one; cut_frag clears what lies past the
+// row.  Three steps, so that all loads of a lane are on their way before one of
+// them is waited for.  NT: past the caches.
 template <typename E, bool VEC, bool NT = false>
 __device__ __forceinline__ uint4 load_frag(const E* row, int k, int width, const E* end) {
+  return k < width && (VEC || row + k + El<E>::EL <= end) ? load_whole<VEC, NT>(row + k) : make_uint4(0, 0, 0, 0);
+}
+template <typename E, bool VEC>
+__device__ __forceinline__ void rest_frag(uint4& v, const E* row, int k, int width, const E* end) {
   constexpr int EL = El<E>::EL;
-  if (VEC)
-    return k < width ? load_whole<true, NT>(row + k) : make_uint4(0, 0, 0, 0);
-  const int left = width - k;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (left <= 0) return v;
-  if (row + k + EL <= end) {
-    v = gld16_u(row + k);
-    if (left < EL) {
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if constexpr (EL == 8) w[q] = left >= 2 * q + 2 ? w[q] : left == 2 * q + 1 ? w[q] & 0xffffu : 0u;
-        else w[q] = left > q ? w[q] : 0u;
-      }
-      v = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    return v;
-  }
+  if (VEC || k >= width || row + k + EL <= end) return;
   E e[EL];
 #pragma unroll
-  for (int i = 0; i < EL; ++i) e[i] = i < left ? gld(row + k + i) : E(0);
-  return __builtin_bit_cast(uint4, e);
+  for (int i = 0; i < EL; ++i) e[i] = k + i < width ? gld(row + k + i) : E(0);
+  v = __builtin_bit_cast(uint4, e);
+}
+template <typename E, bool VEC>
+__device__ __forceinline__ void cut_frag(uint4& v, int left) {
+  if (VEC || left >= El<E>::EL) return;
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (El<E>::EL == 8) w[q] = left >= 2 * q + 2 ? w[q] : left == 2 * q + 1 ? w[q] & 0xffffu : 0u;
+    else w[q] = left > q ? w[q] : 0u;
+  }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// the three at once: what the expand's few pieces of B want (64 tokens of 64 requests,
+// ranks 16 to 64, 2048 -> 5632: 20.7 us against 21.5 us in three steps; the shrink's
+// chunks of the same sets 14.3 us in three steps against 15.7 us at once)
+template <typename E, bool VEC>
+__device__ __forceinline__ uint4 load_cut(const E* row, int k, int width, const E* end) {
+  constexpr int EL = El<E>::EL;
+  if (VEC) return load_frag<E, VEC>(row, k, width, end);
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (k >= width) return v;
+  if (row + k + EL <= end) {
+    v = gld16_u(row + k);
+    cut_frag<E, VEC>(v, width - k);
+  } else {
+    rest_frag<E, VEC>(v, row, k, width, end);
+  }
+  return v;
 }
 
 // ---- shrink: T of each tile, fp32, as the expand's lanes hold it ("frags"):
@@ -146,7 +165,9 @@ __device__ __forceinline__ uint4 load_frag(const E* row, int k, int width, const
 // straight from memory, 16 rows of 64 bytes an instruction, took 1.4 to 1.7 times
 // as long (rows a power of two apart lie in the same channel of the caches, and
 // all workgroups ask for the same columns at once): 8192 rows of 11008 47.8 us
-// against 33.3 us, the rows read in order (without products).
+// against 33.3 us, the rows read in order (without products).  Now: x and dy of
+// 8192 x (4096 + 11008) 50 us, 4.9 TB/s (HBM); with few tokens the chain of segment
+// search, table, chunk and sums, 7 us.
 struct ShrinkJob {
   const void* X;      // [N][width], rows ldx apart
   float* T;           // [parts][tiles][rpmax * 32]
@@ -230,6 +251,7 @@ __device__ __forceinline__ i16x4 ds_read_tr16a(const uint16_t* p) {
 }
 
 // At [column][rp] of each adapter, the ranks past r zero: with it dx is an expand
+// like y.  Workgroups of the shrink's launch do it beside the tiles.
 template <typename E>
 __device__ __forceinline__ void turn_a(const AdEntry* table, const TurnArgs& p, int b, char* lds_raw) {
   E* lds = reinterpret_cast<E*>(lds_raw);
@@ -325,11 +347,38 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
         wr[i] = whole ? load_whole<VEC, false>(r + k) : load_frag<E, VEC>(r, k, J.width, wend);
       }
     }
+    if (VEC) return;
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) {
+        const int c = i * THREADS + tid, row = c / PR;
+        rest_frag<E, VEC>(xr[i], X + (int64_t)(row < tile.rows ? row : 0) * J.ldx, k0 + c % PR * EL, J.width, xend);
+      }
+    }
+    if (USEB ? k0 + CW + EL > J.width : !whole) {
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        if constexpr (USEB) {
+          const int j = k0 + brow[i];
+          if (brow[i] < CW && j < J.width) rest_frag<E, VEC>(wr[i], W + (int64_t)j * ad.r + rank0, bcol[i], rw, wend);
+        } else {
+          const int c = i * THREADS + tid, rank = rank0 + c / PR;
+          rest_frag<E, VEC>(wr[i], W + (int64_t)(rank < ad.r ? rank : 0) * J.width, k0 + c % PR * EL, J.width, wend);
+        }
+      }
+    }
   };
   const int k_end = (part + 1) * a.pw < J.width ? (part + 1) * a.pw : J.width;
   int k0 = part * a.pw;
   load(k0);
   for (;;) {
+    if (!VEC && k0 + CW > J.width) {   // of a piece of B past its ranks only sums that are dropped take anything
+#pragma unroll
+      for (int i = 0; i < NX; ++i) cut_frag<E, VEC>(xr[i], J.width - k0 - (i * THREADS + tid) % PR * EL);
+#pragma unroll
+      for (int i = 0; i < NW; ++i)
+        if (!USEB) cut_frag<E, VEC>(wr[i], J.width - k0 - (i * THREADS + tid) % PR * EL);
+    }
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       const int c = i * THREADS + tid;
@@ -518,13 +567,14 @@ __device__ __forceinline__ uint4 add_frag(uint4 y, const float* v) {
 // follow one another in the grid.  Small workgroups in the order of the memory
 // are what in-place updates of Y want: runs of four tiles a workgroup, with W kept
 // in registers and the next tile's Y fetched ahead, took 48.6 us where one
-// tile a workgroup takes 40.6 us (8192 x 5632, rank 16; 128 columns a wave, whose
-// T is a quarter of the Y it moves; with 64 columns 43.0 us, with 32 46.9 us).
+// tile a workgroup takes 40.4 us, 4.6 TB/s (8192 x 5632, rank 16; 128 columns a wave,
+// whose T is a quarter of the Y it moves; with 64 columns 43.0 us, with 32 46.9 us).
+// The update of Y alone, without T and W, takes 38.8 us.
 // The MFMA's rows are the wave's columns, in an order that gives each lane EL
 // neighbouring columns of a token, and the four lanes of a token neighbouring
 // 16-byte pieces.
 // MFMAs across a wave's columns, 16 columns each:
-constexpr int expand_nc(int rt) { return rt == 1 ? 8 : 4; }
+constexpr int expand_nc(int rt, bool narrow) { return narrow && rt < 16 ? 2 : rt == 1 ? 8 : 4; }
 
 // T's operands of contraction step kk from LDS; PACK: lane groups 0, 1 hold half
 // 0 of the tile's tokens, 2, 3 half 1
@@ -615,10 +665,10 @@ struct Columns {
   }
 };
 
-template <typename E, int RT, bool VECY, bool VECW>
+template <typename E, int RT, bool NARROW, bool VECY, bool VECW>
 __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a) {
   using Op = Operands<E, RT>;
-  constexpr int EL = El<E>::EL, KF = El<E>::KF, NK = Op::NK, NC = expand_nc(RT);
+  constexpr int EL = El<E>::EL, KF = El<E>::KF, NK = Op::NK, NC = expand_nc(RT, NARROW);
   constexpr int KU = RT <= 4 ? NK : 1;   // contraction steps whose W is in flight together
   __shared__ __align__(16) float tl[RT * 512];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -681,7 +731,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs a)
       for (int c = 0; c < NC; ++c) {
         int j = jb + out.col(c, l16);
         j = j < a.width ? j : a.width - 1;
-        wf[u][c] = load_frag<E, VECW>(W + (int64_t)j * in.ldw, (k0 + u) * KF + kc, in.ldw, wend);
+        wf[u][c] = load_cut<E, VECW>(W + (int64_t)j * in.ldw, (k0 + u) * KF + kc, in.ldw, wend);
       }
   };
   load_w(0);
@@ -757,6 +807,16 @@ __global__ __launch_bounds__(64 * SMALL_WAVES) void adapter_small_kernel(const S
         j = j < a.m ? j : a.m - 1;
         wf[u][c] = load_frag<E, VEC>(W + (int64_t)j * ad.r, u * KF + Op::rank0(g), ad.r, W + (int64_t)a.m * ad.r);
       }
+    if (!VEC && jb + 64 + EL > a.m) {
+#pragma unroll
+      for (int u = 0; u < NK; ++u)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          int j = jb + out.col(c, l16);
+          j = j < a.m ? j : a.m - 1;
+          rest_frag<E, VEC>(wf[u][c], W + (int64_t)j * ad.r, u * KF + Op::rank0(g), ad.r, W + (int64_t)a.m * ad.r);
+        }
+    }
   }
   const E* A = static_cast<const E*>(ad.A);
   const E* aend = A + (int64_t)ad.r * a.n;
@@ -787,6 +847,24 @@ __global__ __launch_bounds__(64 * SMALL_WAVES) void adapter_small_kernel(const S
           af[u][i][h] = load_frag<E, VEC>(A + (int64_t)(rank < ad.r ? rank : 0) * a.n, k, a.n, aend);
         }
       }
+    if (!VEC && k0 + ((U - 1) * SMALL_WAVES + 1) * STEP > a.n) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = k0 + u * SMALL_WAVES * STEP + h * KF + g * EL;
+          rest_frag<E, VEC>(xf[u][0][h], x[0], k, a.n, xend);
+          if (halves == 2) rest_frag<E, VEC>(xf[u][1][h], x[1], k, a.n, xend);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) cut_frag<E, VEC>(xf[u][s][h], a.n - k);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const int rank = 16 * i + l16;
+            rest_frag<E, VEC>(af[u][i][h], A + (int64_t)(rank < ad.r ? rank : 0) * a.n, k, a.n, aend);
+            cut_frag<E, VEC>(af[u][i][h], a.n - k);
+          }
+        }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -819,6 +897,8 @@ __global__ __launch_bounds__(64 * SMALL_WAVES) void adapter_small_kernel(const S
   for (int kk = 0; kk < NK; ++kk) {
     uint4 tf[2][Op::NP];
     Op::load(tl, kk, lane, tf);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) cut_frag<E, VEC>(wf[kk][c], ad.r - kk * KF - Op::rank0(g));
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -856,7 +936,8 @@ struct OuterArgs {
 // (a run begins where the one before it ended, so no two pairs share a
 // slot); a second kernel adds an adapter's slots in order.  A slot is written
 // and read as fp32, rank x (n + m): with a run for each wave those bytes
-// outweighed the activations (the same case: 32.8 us).
+// outweighed the activations (the same case: 32.8 us).  8192 x (4096 + 11008), rank
+// 16: 54 us, 4.5 TB/s, HBM; 2001 x 4096, rank 64: 15 us.
 template <typename E, bool VEC, bool NT>
 __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
   constexpr int EL = El<E>::EL, COLS = 16 * EL, LD = COLS + 4;
@@ -888,6 +969,12 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
       const E* row = X + (int64_t)t * J.ldx;
       x[i] = make_uint4(0, 0, 0, 0);
       if (t < en.y) x[i] = whole ? load_whole<VEC, NT>(row + col) : load_frag<E, VEC, NT>(row, col, J.width, xend);
+    }
+    if (VEC || whole) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = BF ? 8 * g + i : 4 * i + g;
+      if (t < en.y) rest_frag<E, VEC>(x[i], X + (int64_t)t * J.ldx, col, J.width, xend);
     }
   };
   while (e0 < e1) {
@@ -973,7 +1060,8 @@ struct ReduceArgs {
 };
 
 // dA [r][n] and dB [m][r] of every adapter; zero where it had no token.  A
-// workgroup takes 64 columns and 16 ranks; dB turns through LDS.
+// workgroup takes 64 columns and 16 ranks; dB turns through LDS.  The slots come out
+// of the caches: 4 to 5 us, the launch for the most part.
 __global__ __launch_bounds__(256) void adapter_reduce_kernel(const ReduceArgs a) {
   __shared__ float turn[64][17];
   const int ad = blockIdx.y, job = blockIdx.z & 1, rank0 = (blockIdx.z >> 1) * 16, width = a.width[job];
@@ -1096,10 +1184,10 @@ AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd,
   p.rpmax = pad_rank(s->max_rank, s->max_rank);
   // the shrink's parts: 1024 columns; with very many workgroups 2048, with few
   // 512; where these are too few still, the ranks are shared out as well
-  // (x is then read again).  Measured with parts of 512, 1024, 1536, 2048, 2560,
-  // 3072 columns: 4099 x 5632 (rank 32) 33.2, 28.8, 27.4, 34.2, 34.9, 33.5 us, 8192 x 2048
-  // -> 5632 58.8, 55.4, 58.0, 57.6, 57.8, 57.7 us, backward of 2001 x 2048 (rank 64) 49.2,
-  // 45.5, 50.3, 50.0, 49.7, 49.3 us, of 8192 x 4096 -> 11008 170, 154, 151, 153, 152, 153 us.
+  // (x is then read again).  Measured with parts of 512, 1024, 1536, 2048, 2560
+  // columns, before later steps: 4099 x 5632 (rank 32) 33.2, 28.8, 27.4, 34.2, 34.9 us,
+  // 8192 x 2048 -> 5632 58.8, 55.4, 58.0, 57.6, 57.8 us, backward of 2001 x 2048 (rank 64)
+  // 49.2, 45.5, 50.3, 50.0, 49.7 us, of 8192 x 4096 -> 11008 170, 154, 151, 153, 152 us.
   const int rt_all = p.rpmax / 16;
   p.rt = rt_all < 4 ? ceil_rt(rt_all) : 4;
   auto groups = [&](int rt) { return (rt_all + rt - 1) / rt; };
@@ -1179,11 +1267,19 @@ void launch_shrink(ShrinkArgs a, const AdPlan& p, int64_t extra, bool vec, bool 
 #undef POETX_RT
 }
 
-template <typename E, int RT>
+// A wave of the expand takes 64 columns, with rank 16 128; where the tiles times the width
+// are at most this, 32: more workgroups, each sooner done.  Measured, 32 against 64 (128)
+// columns: rank 16, 1024 x 2048 11.1 us against 11.9 us, 2048 x 2048 14.7, 15.7, fp32 backward
+// of 333 x 600 20.6, 22.9; rank 32, 4099 x 2048 26.9, 28.3; rank 64, 4096 x 2048 24.1, 24.9; rank
+// 128, 2048 x 2048 22.4, 24.8.  Above: rank 32, 8192 x 5632 64.1 us against 57.8 us, rank 64 85.3,
+// 81.1, rank 128 121, 111.  Above rank 128 always 64 (rank 256, 2048 x 4096: 64.3 us with 32, 54.7 us with 64).
+constexpr int64_t NARROW_WORK = 400 << 10;
+
+template <typename E, int RT, bool NARROW>
 void expand(const ExpandArgs& a, dim3 grid, bool vecy, bool vecw, hipStream_t s) {
-  if (vecy && vecw) hipLaunchKernelGGL((adapter_expand_kernel<E, RT, true, true>), grid, dim3(256), 0, s, a);
-  else if (vecy) hipLaunchKernelGGL((adapter_expand_kernel<E, RT, true, false>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((adapter_expand_kernel<E, RT, false, false>), grid, dim3(256), 0, s, a);
+  if (vecy && vecw) hipLaunchKernelGGL((adapter_expand_kernel<E, RT, NARROW, true, true>), grid, dim3(256), 0, s, a);
+  else if (vecy) hipLaunchKernelGGL((adapter_expand_kernel<E, RT, NARROW, true, false>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((adapter_expand_kernel<E, RT, NARROW, false, false>), grid, dim3(256), 0, s, a);
 }
 template <typename E>
 void launch_expand(ExpandArgs a, const AdPlan& p, bool vecw, hipStream_t s) {
@@ -1192,16 +1288,18 @@ void launch_expand(ExpandArgs a, const AdPlan& p, bool vecw, hipStream_t s) {
   a.info = p.info;
   a.rpmax = p.rpmax;
   a.tiles = (int)p.tiles;
-  const int rt = ceil_rt(p.rpmax / 16), wide = 64 * expand_nc(rt);
+  const int rt = ceil_rt(p.rpmax / 16);
+  const bool narrow = p.tiles * a.width <= NARROW_WORK;
+  const int wide = 64 * expand_nc(rt, narrow);
   a.cols = a.Y ? (a.width + wide - 1) / wide : 0;
   const dim3 grid = tile_grid(a.cols + (a.rows[0] ? 2 : 0), p.tiles);
-  switch (rt) {
-    case 1: expand<E, 1>(a, grid, vecy, vecw, s); break;
-    case 2: expand<E, 2>(a, grid, vecy, vecw, s); break;
-    case 4: expand<E, 4>(a, grid, vecy, vecw, s); break;
-    case 8: expand<E, 8>(a, grid, vecy, vecw, s); break;
-    case 16: expand<E, 16>(a, grid, vecy, vecw, s); break;
-  }
+#define POETX_RT(R) \
+  case R: \
+    if (narrow && R < 16) expand<E, R, R < 16>(a, grid, vecy, vecw, s); \
+    else expand<E, R, false>(a, grid, vecy, vecw, s); \
+    break;
+  switch (rt) { POETX_RT(1) POETX_RT(2) POETX_RT(4) POETX_RT(8) POETX_RT(16) }
+#undef POETX_RT
 }
 
 // Whether the forward goes in one launch: each workgroup then reads its

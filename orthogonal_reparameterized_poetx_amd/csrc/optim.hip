@@ -344,6 +344,8 @@ __device__ __forceinline__ void moments16(const uint8_t* codes, const uint8_t* e
   stg16(out + at + 8, make_uint4(o[4], o[5], o[6], o[7]));
 }
 
+// Both moments as bf16, 16 values a thread: 6 bytes a value, HBM (135.6 M values 158 us,
+// 5.1 TB/s).
 __global__ __launch_bounds__(256) void moments_kernel(const uint8_t* m, const uint8_t* v, const uint8_t* me,
                                                       const uint8_t* ve, uint16_t* mo, uint16_t* vo, int64_t blocks) {
   const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 16;
