@@ -317,3 +317,23 @@ def test_refusals():
     big = torch.zeros(257, 96, dtype=torch.bfloat16, device=d)
     with pytest.raises(P.PoetxError):
         P.AdapterSet(64, 96, [big], [torch.zeros(64, 257, dtype=torch.bfloat16, device=d)], [1.0])
+
+
+@pytest.mark.parametrize("ranks", [[32, 29], [64, 33], [128, 61], [256, 100]])
+def test_wide_waves_of_an_expand(ranks):
+    """Tiles enough for waves of 64 columns at every rank; an odd rank beside a whole one, widths past whole chunks."""
+    c = Case(2504, 600, ranks, [0, 2000, 2003, 5403], [0, -1, 1], 5403, seed=sum(ranks))
+    check_forward(c)
+    check_backward(c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n", [(1, 9), (3, 5), (9, 2), (8, 33), (35, 1)])
+def test_pieces_at_the_end_of_a_matrix(m, n, dtype):
+    """Widths and ranks of a few elements: 16-byte pieces then span several rows and the matrix's end."""
+    c = Case(m, n, [1, 2, 3, 7], [0, 3, 4, 40, 41], [0, 1, 2, 3], 41, dtype=dtype, seed=10 * m + n)
+    check_forward(c)
+    check_backward(c)
+    c = Case(m, n, [33, 20], [0, 3, 41], [0, 1], 41, dtype=dtype, seed=10 * m + n + 1)
+    check_forward(c)
+    check_backward(c)
