@@ -251,7 +251,9 @@ __device__ __forceinline__ i16x4 ds_read_tr16a(const uint16_t* p) {
 }
 
 // At [column][rp] of each adapter, the ranks past r zero: with it dx is an expand
-// like y.  Workgroups of the shrink's launch do it beside the tiles.
+// like y.  Workgroups of the shrink's launch do it beside the tiles, in whole rows of
+// its grid (with one to a row, the others empty, the backward of 2001 x 2048, rank
+// 64, took 42.9 us instead of 39.8 us).
 template <typename E>
 __device__ __forceinline__ void turn_a(const AdEntry* table, const TurnArgs& p, int b, char* lds_raw) {
   E* lds = reinterpret_cast<E*>(lds_raw);
@@ -462,8 +464,8 @@ __global__ __launch_bounds__(64 * SHRINK_WAVES) void adapter_shrink_kernel(const
   __shared__ __align__(16) char lds[shrink_lds(RT, sizeof(E))];
   const int64_t w = (int64_t)blockIdx.z * TILES_Y + blockIdx.y;
   if (w >= a.tiles) {
-    const int64_t x = w - a.tiles;
-    if (blockIdx.x || !a.lists.list) return;
+    const int64_t x = (w - a.tiles) * gridDim.x + blockIdx.x;
+    if (!a.lists.list) return;
     if (x < a.seg.count) build_list<64 * SHRINK_WAVES>(a.seg, a.lists, (int)x, reinterpret_cast<int*>(lds));
     else if (a.turn.At && x - a.seg.count < (int64_t)a.seg.count * a.turn.per)
       turn_a<E>(a.table, a.turn, (int)(x - a.seg.count), lds);
@@ -1255,7 +1257,8 @@ void launch_shrink(ShrinkArgs a, const AdPlan& p, int64_t extra, bool vec, bool 
   a.info = p.info;
   a.pw = p.pw;
   a.groups = p.rgroups;
-  const dim3 grid = tile_grid((p.parts[0] + p.parts[1]) * p.rgroups, p.tiles + extra);
+  const int64_t x = (p.parts[0] + p.parts[1]) * p.rgroups;
+  const dim3 grid = tile_grid(x, p.tiles + (extra + x - 1) / x);
   const dim3 block(64 * SHRINK_WAVES);
 #define POETX_RT(R) \
   case R: \
