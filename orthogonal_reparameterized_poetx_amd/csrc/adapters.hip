@@ -15,10 +15,10 @@
 #include "../../include/poetx.h"
 #include "global.h"
 #include "host.h"
+#include "shrink.h"
 
 namespace poetx {
 
-constexpr int AD_T = 32;          // tokens of a tile
 constexpr int AD_MAX_RANK = 256;
 
 struct AdEntry {
@@ -279,21 +279,6 @@ __device__ __forceinline__ void turn_a(const AdEntry* table, const TurnArgs& p, 
   }
 }
 
-constexpr int SHRINK_WAVES = 4;
-constexpr int TURN_LDS = 16 * 1024;   // bytes a transpose may take
-// a chunk: bytes of a row; LDS bytes of a row of x or A, of x, of the weights
-constexpr int shrink_rb(int rt) { return rt == 1 ? 1024 : 512; }
-constexpr int shrink_row(int rt) { return shrink_rb(rt) + 16; }
-constexpr int shrink_x(int rt) { return AD_T * shrink_row(rt); }
-constexpr int shrink_w(int rt, int es) {
-  const int byA = 16 * rt * shrink_row(rt), byB = shrink_rb(rt) / es * (16 * rt + (es == 4 ? 4 : 0)) * es;
-  return byA > byB ? byA : byB;
-}
-constexpr int shrink_lds(int rt, int es) {
-  const int most = shrink_x(rt) + shrink_w(rt, es);
-  return most > TURN_LDS ? most : TURN_LDS;
-}
-
 template <typename E, int RT, bool VEC, bool NT, bool USEB>
 __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob& J, const AdTile& tile, int w,
                                             int group, int part, char* lds) {
@@ -307,6 +292,25 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
   const int rank0 = group * RT * 16;
   if (rank0 >= ad.rp) return;
   const int rt_n = (ad.rp - rank0) >> 4;   // rank tiles of this adapter from rank0 on
+  // value of rank tile i and half s that this thread stores
+  auto put = [&](int i, int s, float v) {
+    float* T = J.T + ((int64_t)part * a.tiles + w) * a.rpmax * AD_T;
+    const int lanes = a.rpmax < KF ? 16 * (a.rpmax / EL) : 64;
+    const int rank = rank0 + 16 * i + 4 * (tid >> 6) + (tid & 3), c = (tid >> 2) & 15;
+    v = rank < ad.r && 16 * s + c < tile.rows ? v * ad.scale : 0.f;
+    const int kk = rank / KF, gg = rank % KF / EL, e = rank % EL;
+    T[((kk * 2 + s) * lanes + gg * 16 + c) * EL + e] = v;
+  };
+  const RankGroup group_of = rank_group(ad.r, rank0, RT, EL);
+  if (group_of.ranks == 0) {   // padding alone: zeros, which the expand multiplies
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      if (i < rt_n) {
+        put(i, 0, 0.f);
+        put(i, 1, 0.f);
+      }
+    return;
+  }
   const E* X = static_cast<const E*>(J.X) + (int64_t)tile.t0 * J.ldx;
   const E* xend = static_cast<const E*>(J.X) + (int64_t)(a.seg.N - 1) * J.ldx + J.width;
   const E* W = static_cast<const E*>(USEB ? ad.B : ad.A);
@@ -314,8 +318,7 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
   E* lx = reinterpret_cast<E*>(lds);
   E* lw = reinterpret_cast<E*>(lds + shrink_x(RT));
   // B: rows of the chunk, the ranks rank0 .. rank0 + rw in rc pieces, ldb elements apart
-  const int rw = ad.r - rank0 < 16 * RT ? ad.r - rank0 : 16 * RT, rc = (rw + EL - 1) / EL;
-  const int ldb = rc * EL + (ES == 4 ? 4 : 0);
+  const int rw = group_of.ranks, rc = group_of.pieces, ldb = group_of.ld;
   int brow[USEB ? NW : 1], bcol[USEB ? NW : 1];
   if constexpr (USEB) {
 #pragma unroll
@@ -434,8 +437,6 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
     if (!more) break;
   }
   float* red = reinterpret_cast<float*>(lds);
-  float* T = J.T + ((int64_t)part * a.tiles + w) * a.rpmax * AD_T;
-  const int lanes = a.rpmax < KF ? 16 * (a.rpmax / EL) : 64;
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     if (i < rt_n) {
@@ -447,10 +448,7 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
         float v = 0.f;
 #pragma unroll
         for (int q = 0; q < SHRINK_WAVES; ++q) v += red[q * 512 + s * 256 + tid];
-        const int rank = rank0 + 16 * i + 4 * (tid >> 6) + (tid & 3), c = (tid >> 2) & 15;
-        v = rank < ad.r && 16 * s + c < tile.rows ? v * ad.scale : 0.f;
-        const int kk = rank / KF, gg = rank % KF / EL, e = rank % EL;
-        T[((kk * 2 + s) * lanes + gg * 16 + c) * EL + e] = v;
+        put(i, s, v);
       }
       __syncthreads();
     }

@@ -337,3 +337,15 @@ def test_pieces_at_the_end_of_a_matrix(m, n, dtype):
     c = Case(m, n, [33, 20], [0, 3, 41], [0, 1], 41, dtype=dtype, seed=10 * m + n + 1)
     check_forward(c)
     check_backward(c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ranks", [[32, 16, 8, 29], [64, 1, 47, 16], [100, 3, 80, 112]])
+@pytest.mark.parametrize("m,n", [(512, 768), (515, 773)])
+def test_rank_groups_in_the_padding(m, n, ranks, dtype):
+    """Few tiles: the ranks are shared out in groups of 16, and those of an adapter whose rank is at least 16 below
+    its padding (to a multiple of 32) end in a group without a rank."""
+    start = [0, 32, 64, 97, 130, 131, 190, 220, 256]
+    c = Case(m, n, ranks, start, [0, 1, 2, 3, 1, 0, 2, 1], 256, dtype=dtype, seed=m + sum(ranks))
+    check_forward(c)
+    check_backward(c)
