@@ -23,7 +23,8 @@ class AdapterSet:
     set or -1), both on the device.
 
     Calls run on the current stream.  Those of one object share its
-    workspaces: on several streams at once, use an object for each.
+    workspaces: on several streams at once, use an object for each.  A
+    captured graph uses the object's buffers: keep the object as long as it.
     """
 
     def __init__(self, m, n, A, B, scales, dA=None, dB=None):
@@ -42,6 +43,7 @@ class AdapterSet:
             self._check("B[%d]" % i, b, (self.m, r), self.dtype)
         self.dA, self.dB = self._grads("dA", dA, self.A), self._grads("dB", dB, self.B)
         self._ws, self._need = {}, {}     # workspaces by op; their sizes by (op, tokens, segments)
+        self._replaced = []               # smaller workspaces of earlier calls
         self._make_table()
 
     def _check(self, name, t, shape, dtype):
@@ -96,6 +98,11 @@ class AdapterSet:
             need = self._need[op, N, nseg] = L.adapters_workspace_bytes(self.aset, N, nseg, op)
         ws = self._ws.get(op)
         if ws is None or ws.numel() < need:
+            # the smaller one stays: a captured graph or another stream's queued work may still use it
+            # (twice its size at least, so that less is kept than is in use)
+            if ws is not None:
+                self._replaced.append(ws)
+                need = max(need, 2 * ws.numel())
             ws = self._ws[op] = L.make_workspace(need, self.device)
         return ws
 

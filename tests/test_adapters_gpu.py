@@ -349,3 +349,40 @@ def test_rank_groups_in_the_padding(m, n, ranks, dtype):
     c = Case(m, n, ranks, start, [0, 1, 2, 3, 1, 0, 2, 1], 256, dtype=dtype, seed=m + sum(ranks))
     check_forward(c)
     check_backward(c)
+
+
+def _fill_freed_memory(torch):
+    """Tensors of many sizes, so that blocks that were given back are in use again, and hold NaN."""
+    return [torch.full((1 << k,), float("nan"), device="cuda:0") for k in range(7, 22) for _ in range(6)]
+
+
+def test_replay_after_a_larger_call():
+    """A server's order: decode captured, a prompt in between that needs a larger workspace, replay."""
+    torch = torch_mod()
+    ranks = [64, 16, 61, 32]
+    c = Case(2048, 1024, ranks, np.arange(49), np.arange(48) % 5 - 1, 48, seed=30)
+    big = Case(2048, 1024, ranks, [0, 1000, 3001], [2, 0], 3001, seed=31)
+    dA, dB = ([torch.zeros(t.shape, device="cuda:0") for t in ts] for ts in (c.A, c.B))
+    aset = c.set(dA=dA, dB=dB)
+    Y0, dX0 = c.Y.clone(), c.dX.clone()
+    Y, dX = Y0.clone(), dX0.clone()
+    aset.forward(c.X, Y, c.sd, c.wd)
+    aset.backward(c.X, c.dY, c.sd, c.wd, dX=dX)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in [Y, dX] + dA + dB]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        aset.forward(c.X, Y, c.sd, c.wd)
+        aset.backward(c.X, c.dY, c.sd, c.wd, dX=dX)
+    for _ in range(3):
+        aset.forward(big.X, big.Y, big.sd, big.wd)
+        aset.backward(big.X, big.dY, big.sd, big.wd, dX=big.dX)
+        torch.cuda.synchronize()
+        held = _fill_freed_memory(torch)
+        Y.copy_(Y0)
+        dX.copy_(dX0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, [Y, dX] + dA + dB))
+        assert all(bool(torch.isnan(t).all()) for t in held)
+        del held

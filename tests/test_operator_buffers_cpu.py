@@ -1,6 +1,8 @@
 """What AdapterSet and AdamW hand to the library: checks of the caller's buffers
 and lifetime of their own, without a GPU."""
 
+import weakref
+
 import pytest
 import torch
 
@@ -45,3 +47,27 @@ def test_moments_of_32_bits_take_no_output(monkeypatch):
     assert opt.moments()[0].dtype == torch.float32
     with pytest.raises(ValueError):
         opt.moments(out=[dev(512), dev(512)])
+
+
+def adapters(P, m=512, n=256, ranks=(16, 8), **kw):
+    return P.AdapterSet(m, n, [dev(r, n, dtype=torch.bfloat16) for r in ranks],
+                        [dev(m, r, dtype=torch.bfloat16) for r in ranks], [1.0] * len(ranks), **kw)
+
+
+@pytest.mark.parametrize("op", ["OP_FORWARD", "OP_BACKWARD"])
+def test_a_replaced_workspace_stays(monkeypatch, op):
+    """A captured graph, or work queued on some stream, may still use the smaller one."""
+    P = package(monkeypatch)
+    s = adapters(P)
+    op = getattr(P, op)
+    live = []
+    for N in (64, 65, 70, 100, 8192, 3000, 9000, 20000):
+        ws = s.workspace(op, N, 3)
+        assert ws.numel() >= P.adapters_workspace_bytes(s.aset, N, 3, op)
+        live.append((weakref.ref(ws), ws.data_ptr()))
+        assert s.workspace(op, 64, 3) is ws         # smaller calls take the one there is
+        del ws
+    assert all(r() is not None for r, _ in live)
+    # what is kept is less than what is in use
+    kept = {p: r().numel() for r, p in live}
+    assert sum(kept.values()) < 2 * max(kept.values())
