@@ -16,7 +16,8 @@ class AdapterSet:
            float32, kept and read in place; ranks 1..256, they may differ
     scales one factor for each adapter
     dA, dB lists of float32 gradients of the same shapes that backward() writes;
-           by default allocated by the first backward()
+           by default allocated by the first backward() (which then cannot
+           be inside a graph capture)
 
     A batch is cut into segments of consecutive tokens: seg_start (int32,
     one more entry than segments) and seg_adapter (int32, an index into the
@@ -44,6 +45,7 @@ class AdapterSet:
         self.dA, self.dB = self._grads("dA", dA, self.A), self._grads("dB", dB, self.B)
         self._ws, self._need = {}, {}     # workspaces by op; their sizes by (op, tokens, segments)
         self._replaced = []               # smaller workspaces of earlier calls
+        self.table = None
         self._make_table()
 
     def _check(self, name, t, shape, dtype):
@@ -67,7 +69,10 @@ class AdapterSet:
                 for a, b, da, db, s in zip(self.A, self.B, self.dA or none, self.dB or none, self.scales)]
         dt = L.POETX_BF16 if self.dtype == torch.bfloat16 else L.POETX_F32
         host, self.aset = L.adapter_table(rows, self.m, self.n, dt)
-        self.table = host.to(self.device)
+        if self.table is None:
+            self.table = host.to(self.device)
+        else:   # in its place: captured graphs hold the address (the pointers of A and B are the same again)
+            self.table.copy_(host)
         self.aset.table = self.table.data_ptr()
         torch.cuda.current_stream(self.device).synchronize()
 
@@ -125,6 +130,8 @@ class AdapterSet:
         if self.dA is None or self.dB is None:
             if accumulate:
                 raise ValueError("accumulate needs gradients to add to")
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("the first backward makes the gradients: call it before the capture, or give dA and dB")
             self.dA = self.dA or [torch.zeros_like(a, dtype=torch.float32) for a in self.A]
             self.dB = self.dB or [torch.zeros_like(b, dtype=torch.float32) for b in self.B]
             self._make_table()

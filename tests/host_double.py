@@ -29,5 +29,6 @@ def package(monkeypatch):
     if not os.path.exists(P.LIB_PATH):
         pytest.skip("libpoetx.so not built")
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(P._lib, "stream_handle", lambda stream: 0)
     return P

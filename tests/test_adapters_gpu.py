@@ -386,3 +386,39 @@ def test_replay_after_a_larger_call():
         assert all(torch.equal(a, b) for a, b in zip(want, [Y, dX] + dA + dB))
         assert all(bool(torch.isnan(t).all()) for t in held)
         del held
+
+
+def test_replay_after_the_first_backward():
+    """A forward captured before the set has gradients."""
+    torch = torch_mod()
+    c = Case(512, 640, [16, 40], [0, 33, 100], [1, 0], 100, seed=32)
+    aset = c.set()
+    Y0 = c.Y.clone()
+    aset.forward(c.X, c.Y, c.sd, c.wd)
+    torch.cuda.synchronize()
+    want = c.Y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        aset.forward(c.X, c.Y, c.sd, c.wd)
+    check_backward(c, aset)
+    held = _fill_freed_memory(torch)
+    for _ in range(3):
+        c.Y.copy_(Y0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c.Y, want)
+        check_backward(c, aset)
+    del held
+
+
+def test_first_backward_inside_a_capture():
+    torch = torch_mod()
+    c = Case(64, 96, [16], [0, 33], [0], 33, seed=33)
+    aset = c.set()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.X.add_(0)
+        with pytest.raises(RuntimeError):
+            aset.backward(c.X, c.dY, c.sd, c.wd)
+    graph.replay()
+    check_backward(c, aset)

@@ -71,3 +71,39 @@ def test_a_replaced_workspace_stays(monkeypatch, op):
     # what is kept is less than what is in use
     kept = {p: r().numel() for r, p in live}
     assert sum(kept.values()) < 2 * max(kept.values())
+
+
+def test_first_backward_leaves_the_table_where_it_is(monkeypatch):
+    """A forward captured before it reads A and B through that table."""
+    P = package(monkeypatch)
+    seen = []
+    monkeypatch.setattr(P._lib, "poetx_adapters_backward", lambda aset, *a: seen.append((aset.table, aset.flags)))
+    s = adapters(P)
+    where, before = s.aset.table, s.table.clone()
+    assert where == s.table.data_ptr()
+    X, dY = dev(40, 256, dtype=torch.bfloat16), dev(40, 512, dtype=torch.bfloat16)
+    seg = dev(2, dtype=torch.int32), dev(1, dtype=torch.int32)
+    dA, dB = s.backward(X, dY, *seg)
+    assert s.table.data_ptr() == where and seen == [(where, 0)]
+    # the same pointers of A and B, now with gradients
+    rows = [t.view(torch.int64).view(len(dA), -1) for t in (before, s.table)]
+    assert torch.equal(rows[0][:, :2], rows[1][:, :2]) and not rows[0][:, 2:4].any()
+    assert rows[1][:, 2].tolist() == [t.data_ptr() for t in dA] and rows[1][:, 3].tolist() == [t.data_ptr() for t in dB]
+    s.backward(X, dY, *seg, accumulate=True)
+    assert seen[1:] == [(where, P.POETX_ACCUMULATE_GRAD)]
+
+
+def test_first_backward_inside_a_capture_is_refused(monkeypatch):
+    """It makes the gradients and copies the table from the host, which a capture cannot hold."""
+    P = package(monkeypatch)
+    seen = []
+    monkeypatch.setattr(P._lib, "poetx_adapters_backward", lambda *a: seen.append(a))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    X, dY = dev(40, 256, dtype=torch.bfloat16), dev(40, 512, dtype=torch.bfloat16)
+    seg = dev(2, dtype=torch.int32), dev(1, dtype=torch.int32)
+    s = adapters(P)
+    with pytest.raises(RuntimeError):
+        s.backward(X, dY, *seg)
+    assert s.dA is None and s.dB is None and not seen
+    adapters(P, dA=[dev(16, 256), dev(8, 256)], dB=[dev(512, 16), dev(512, 8)]).backward(X, dY, *seg)
+    assert len(seen) == 1
