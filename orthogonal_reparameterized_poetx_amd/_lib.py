@@ -233,6 +233,8 @@ def stream_handle(stream):
         if get is not None:     # without the Stream object (3 us less)
             return get(torch.cuda.current_device())
         return int(torch.cuda.current_stream().cuda_stream)
+    if type(stream) is int:
+        return stream
     if hasattr(stream, "cuda_stream"):
         return int(stream.cuda_stream)
     return int(stream)
@@ -276,9 +278,56 @@ def poetx_transpose_w0(layer, W0p, stream=None):
     _check("poetx_transpose_w0", lib().poetx_transpose_w0(ctypes.byref(layer), _ptr(W0p), _stream(stream)))
 
 
-def make_workspace(nbytes, device):
+def make_workspace(nbytes, device, stream=None):
+    """A buffer for calls on `stream` (as stream_handle takes it), from that stream's memory."""
     import torch
-    return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
+        return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+
+
+class Owned:
+    """Device buffers of an object whose calls may run on several streams.
+
+    They live as long as the object, and torch's allocator is told of each
+    stream that uses them: once the object is gone it hands none of them out
+    before that stream's queued work is done.  (Not of a stream that is given
+    as a raw handle, which may be gone by then: keep the object until its work
+    is done.)"""
+
+    def __init__(self, *buffers):
+        self._buffers, self._streams = list(buffers), {}
+
+    def add(self, t):
+        self._buffers.append(t)
+        for s in self._streams.values():
+            if s is not None:
+                t.record_stream(s)
+        return t
+
+    def handle(self, stream):
+        """Raw handle of a call's stream."""
+        h = stream_handle(stream)
+        if h not in self._streams:
+            import torch
+            s = self._streams[h] = torch.cuda.current_stream() if stream is None else \
+                stream if hasattr(stream, "cuda_stream") else None
+            if s is not None:
+                for t in self._buffers:
+                    t.record_stream(s)
+        return h
+
+
+def lend(tensors, stream):
+    """Tensors just made on the current stream, for a call on `stream`."""
+    import torch
+    if stream is None:
+        return
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+    s.wait_stream(torch.cuda.current_stream())
+    for t in tensors:
+        t.record_stream(s)
 
 
 def poetx_build_blocks(theta, nblocks, b, Q32=None, Qbf16=None, QTbf16=None, ws=None, stream=None):

@@ -44,7 +44,6 @@ class AdapterSet:
             self._check("B[%d]" % i, b, (self.m, r), self.dtype)
         self.dA, self.dB = self._grads("dA", dA, self.A), self._grads("dB", dB, self.B)
         self._ws, self._need = {}, {}     # workspaces by op; their sizes by (op, tokens, segments)
-        self._replaced = []               # smaller workspaces of earlier calls
         self.table = None
         self._make_table()
 
@@ -71,6 +70,7 @@ class AdapterSet:
         host, self.aset = L.adapter_table(rows, self.m, self.n, dt)
         if self.table is None:
             self.table = host.to(self.device)
+            self._owned = L.Owned(self.table)
         else:   # in its place: captured graphs hold the address (the pointers of A and B are the same again)
             self.table.copy_(host)
         self.aset.table = self.table.data_ptr()
@@ -95,7 +95,7 @@ class AdapterSet:
             raise ValueError("seg_start needs one entry more than seg_adapter")
         return seg_adapter.numel()
 
-    def workspace(self, op, N, nseg):
+    def workspace(self, op, N, nseg, stream=None):
         need = self._need.get((op, N, nseg))
         if need is None:
             if len(self._need) > 4096:
@@ -106,9 +106,8 @@ class AdapterSet:
             # the smaller one stays: a captured graph or another stream's queued work may still use it
             # (twice its size at least, so that less is kept than is in use)
             if ws is not None:
-                self._replaced.append(ws)
                 need = max(need, 2 * ws.numel())
-            ws = self._ws[op] = L.make_workspace(need, self.device)
+            ws = self._ws[op] = self._owned.add(L.make_workspace(need, self.device, stream))
         return ws
 
     def forward(self, X, Y, seg_start, seg_adapter, stream=None):
@@ -116,8 +115,9 @@ class AdapterSet:
         nseg = self._segs(seg_start, seg_adapter)
         N = X.shape[0]
         ldx, ldy = self._rows("X", X, self.n), self._rows("Y", Y, self.m, N)
+        handle = self._owned.handle(stream)
         L.poetx_adapters_forward(self.aset, seg_start, seg_adapter, nseg, X, ldx, N, Y, ldy,
-                                 self.workspace(L.OP_FORWARD, N, nseg), stream)
+                                 self.workspace(L.OP_FORWARD, N, nseg, stream), handle)
         return Y
 
     def backward(self, X, dY, seg_start, seg_adapter, dX=None, accumulate=False, stream=None):
@@ -134,8 +134,9 @@ class AdapterSet:
                 raise RuntimeError("the first backward makes the gradients: call it before the capture, or give dA and dB")
             self.dA = self.dA or [torch.zeros_like(a, dtype=torch.float32) for a in self.A]
             self.dB = self.dB or [torch.zeros_like(b, dtype=torch.float32) for b in self.B]
-            self._make_table()
+            self._make_table()      # waits for the current stream: the gradients are there for any
         self.aset.flags = L.POETX_ACCUMULATE_GRAD if accumulate else 0
+        handle = self._owned.handle(stream)
         L.poetx_adapters_backward(self.aset, seg_start, seg_adapter, nseg, X, ldx, dY, lddy, N, dX, lddx,
-                                  self.workspace(L.OP_BACKWARD, N, nseg), stream)
+                                  self.workspace(L.OP_BACKWARD, N, nseg, stream), handle)
         return self.dA, self.dB

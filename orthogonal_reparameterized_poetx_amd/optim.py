@@ -70,10 +70,11 @@ class GradNorm:
         self.out = torch.zeros(2, dtype=torch.float32, device=self.device)
         self.ws = L.make_workspace(L.grad_norm_workspace_bytes(self.pset), self.device)
         self._views = self.out[0], self.out[1]
+        self._owned = L.Owned(self.table, self.out, self.ws)
         torch.cuda.current_stream(self.device).synchronize()
 
     def __call__(self, max_norm=float("inf"), stream=None):
-        L.poetx_grad_norm(self.pset, max_norm, self.out, self.ws, stream)
+        L.poetx_grad_norm(self.pset, max_norm, self.out, self.ws, self._owned.handle(stream))
         return self._views
 
 
@@ -113,6 +114,7 @@ class AdamW:
         self._cstate = L.AdamwState(L._addr(self._state["m"]), L._addr(self._state["v"]),
                                     L._addr(self._state.get("m_exp")), L._addr(self._state.get("v_exp")),
                                     L.POETX_STATE_8BIT if state_bits == 8 else L.POETX_STATE_F32, 0)
+        self._owned = L.Owned(self.table, *self._state.values())
         self._norm = None
         torch.cuda.current_stream(self.device).synchronize()
 
@@ -139,7 +141,7 @@ class AdamW:
         gradient is multiplied by (nothing is written where it is not finite)."""
         if coef is not None and (coef.numel() != 1 or coef.dtype != torch.float32 or coef.device != self.device):
             raise ValueError("coef must be one float32 value on %s" % self.device)
-        L.poetx_adamw_step(self.pset, self._cstate, self.hyper, self.steps + 1, coef, stream)
+        L.poetx_adamw_step(self.pset, self._cstate, self.hyper, self.steps + 1, coef, self._owned.handle(stream))
         self.steps += 1
 
     def moments(self, out=None, stream=None):
@@ -153,11 +155,12 @@ class AdamW:
             return self._state["m"], self._state["v"]
         if out is None:
             out = [torch.empty(n, dtype=torch.bfloat16, device=self.device) for _ in range(2)]
+            L.lend(out, stream)
         if len(out) != 2:
             raise ValueError("out is a pair, for m and v")
         for name, t in zip("mv", out):
             if t is not None and (_flat(t, "output of " + name, self.device).dtype != torch.bfloat16 or t.numel() != n):
                 raise ValueError("output of %s must be bfloat16 with %d values" % (name, n))
         m, v = out
-        L.poetx_adamw_moments(self.pset, self._cstate, m, v, stream)
+        L.poetx_adamw_moments(self.pset, self._cstate, m, v, self._owned.handle(stream))
         return m, v

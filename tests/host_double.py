@@ -30,5 +30,6 @@ def package(monkeypatch):
         pytest.skip("libpoetx.so not built")
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
     monkeypatch.setattr(P._lib, "stream_handle", lambda stream: 0)
     return P

@@ -422,3 +422,55 @@ def test_first_backward_inside_a_capture():
             aset.backward(c.X, c.dY, c.sd, c.wd)
     graph.replay()
     check_backward(c, aset)
+
+
+def test_growth_on_another_stream():
+    """A first and a larger call on a stream of their own, while the current stream's queued work still writes
+    memory that it has given back."""
+    torch = torch_mod()
+    small = Case(512, 640, [16, 40], [0, 33, 100], [1, 0], 100, seed=34)
+    big = Case(512, 640, [16, 40], [0, 333, 2000], [1, 0], 2000, seed=34)
+    side = torch.cuda.Stream()
+    want = []
+    for c in (small, big):      # (one set for both: the adapters of the larger case)
+        Y = c.Y.clone()
+        big.set().forward(c.X, Y, c.sd, c.wd)
+        want.append(Y)
+    x = torch.randn(4096, 4096, device="cuda:0")
+    for handle in (side, side.cuda_stream):
+        aset = big.set()
+        for c, w in zip((small, big), want):
+            Y = c.Y.clone()
+            torch.cuda.synchronize()
+            junk = [torch.empty(1 << k, dtype=torch.uint8, device="cuda:0") for k in range(12, 24)]
+            for _ in range(20):
+                x = (x @ x).clamp(-1, 1)                     # the current stream is busy
+            for t in junk:
+                t.fill_(255)
+            where = [(t.data_ptr(), t.data_ptr() + t.numel()) for t in junk]
+            del junk, t
+            aset.forward(c.X, Y, c.sd, c.wd, stream=handle)
+            ws = aset.workspace(0, c.N, len(c.which))
+            assert all(ws.data_ptr() + ws.numel() <= lo or hi <= ws.data_ptr() for lo, hi in where)
+            torch.cuda.synchronize()
+            assert torch.equal(Y, w)
+
+
+def test_object_gone_while_its_stream_is_busy():
+    torch = torch_mod()
+    c = Case(512, 640, [16, 40], [0, 33, 1000], [1, 0], 1000, seed=35)
+    Y, want = c.Y.clone(), c.Y.clone()
+    c.set().forward(c.X, want, c.sd, c.wd)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    x = torch.randn(4096, 4096, device="cuda:0")
+    torch.cuda.synchronize()
+    aset = c.set()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            x = (x @ x).clamp(-1, 1)
+    aset.forward(c.X, Y, c.sd, c.wd, stream=side)
+    del aset
+    held = _fill_freed_memory(torch)                         # on the current stream, at once
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want) and all(bool(torch.isnan(t).all()) for t in held)

@@ -1,12 +1,13 @@
 """What AdapterSet and AdamW hand to the library: checks of the caller's buffers
 and lifetime of their own, without a GPU."""
 
+import contextlib
 import weakref
 
 import pytest
 import torch
 
-from host_double import dev, package
+from host_double import OnHost, dev, package
 
 
 def adamw(P, n, bits):
@@ -107,3 +108,90 @@ def test_first_backward_inside_a_capture_is_refused(monkeypatch):
     assert s.dA is None and s.dB is None and not seen
     adapters(P, dA=[dev(16, 256), dev(8, 256)], dB=[dev(512, 16), dev(512, 8)]).backward(X, dY, *seg)
     assert len(seen) == 1
+
+
+class Side:
+    def __init__(self, handle):
+        self.cuda_stream, self.waits = handle, []
+
+    def synchronize(self):
+        pass
+
+    def wait_stream(self, other):
+        self.waits.append(other)
+
+
+def streams(monkeypatch):
+    """The package, the streams that each buffer is recorded on, and the stream that each workspace is made on."""
+    P = package(monkeypatch)
+    current, recorded, made, context = Side(0), [], {}, [None]
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Side)
+    monkeypatch.setattr(P._lib, "stream_handle",
+                        lambda s: 0 if s is None else s if isinstance(s, int) else s.cuda_stream)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s.cuda_stream)))
+    monkeypatch.setattr(P._lib, "poetx_adapters_forward", lambda *a: None)
+    monkeypatch.setattr(P._lib, "poetx_adapters_backward", lambda *a: None)
+    monkeypatch.setattr(P._lib, "poetx_adamw_step", lambda *a: None)
+    monkeypatch.setattr(P._lib, "poetx_grad_norm", lambda *a: None)
+    monkeypatch.setattr(P._lib, "poetx_adamw_moments", lambda *a: None)
+
+    @contextlib.contextmanager
+    def on(s):
+        context.append(s)
+        yield
+        context.pop()
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    real = torch.empty
+
+    def note(*a, **kw):
+        t = real(*a, **kw).as_subclass(OnHost)
+        made[t.data_ptr()] = context[-1] and context[-1].cuda_stream
+        return t
+    monkeypatch.setattr(torch, "empty", note)
+    return P, current, recorded, made
+
+
+def test_buffers_of_an_adapter_set_know_their_streams(monkeypatch):
+    P, current, recorded, made = streams(monkeypatch)
+    s = adapters(P)
+    X, Y = dev(40, 256, dtype=torch.bfloat16), dev(40, 512, dtype=torch.bfloat16)
+    seg = dev(2, dtype=torch.int32), dev(1, dtype=torch.int32)
+    a = Side(7)
+    s.forward(X, Y, *seg, stream=a)
+    ws = s.workspace(P.OP_FORWARD, 40, 1)
+    # made where it is first used: the current stream's queued work may still hold what it gave back
+    assert made[ws.data_ptr()] == 7
+    assert (s.table.data_ptr(), 7) in recorded
+    # used on a second stream
+    s.forward(X, Y, *seg)
+    assert (ws.data_ptr(), 0) in recorded
+    n = len(recorded)
+    for _ in range(3):
+        s.forward(X, Y, *seg)
+        s.forward(X, Y, *seg, stream=a)
+    assert len(recorded) == n            # known: nothing more to do
+    # a workspace that is made later knows both
+    s.backward(X, Y, *seg, stream=a)
+    wb = s.workspace(P.OP_BACKWARD, 40, 1)
+    assert made[wb.data_ptr()] == 7 and (wb.data_ptr(), 0) in recorded
+    # a raw handle may be gone when the buffers are given back: made there, not recorded
+    s.forward(dev(4000, 256, dtype=torch.bfloat16), dev(4000, 512, dtype=torch.bfloat16), *seg, stream=9)
+    ws = s.workspace(P.OP_FORWARD, 4000, 1)
+    assert made[ws.data_ptr()] == 9 and not [r for r in recorded if r[1] == 9]
+
+
+def test_buffers_of_the_optimizer_know_their_streams(monkeypatch):
+    P, current, recorded, made = streams(monkeypatch)
+    a = Side(7)
+    opt = adamw(P, 300, 8)
+    opt.step(stream=a)
+    assert {(t.data_ptr(), 7) for t in [opt.table, *opt.state().values()]} <= set(recorded)
+    norm = P.GradNorm([dev(300)])
+    norm(1.0, stream=a)
+    assert {(t.data_ptr(), 7) for t in (norm.table, norm.ws, norm.out)} <= set(recorded)
+    # outputs made for another stream's call: it waits for the work of the stream they come from
+    m, v = opt.moments(stream=a)
+    assert a.waits == [current] and {(m.data_ptr(), 7), (v.data_ptr(), 7)} <= set(recorded)
+    opt.moments()
+    assert a.waits == [current]
