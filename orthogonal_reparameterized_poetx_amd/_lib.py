@@ -224,15 +224,21 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_current = None     # torch's functions for the current stream's handle, looked up once
+
+
 def stream_handle(stream):
     """The raw hipStream_t (an int) of a torch.cuda.Stream, a raw handle
     given as an int, or None (torch's current stream)."""
     if stream is None:
-        import torch
-        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        global _current
+        if _current is None:
+            import torch
+            _current = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda
+        get, cuda = _current
         if get is not None:     # without the Stream object (3 us less)
-            return get(torch.cuda.current_device())
-        return int(torch.cuda.current_stream().cuda_stream)
+            return get(cuda.current_device())
+        return int(cuda.current_stream().cuda_stream)
     if type(stream) is int:
         return stream
     if hasattr(stream, "cuda_stream"):
@@ -320,10 +326,8 @@ class Owned:
 
 
 def lend(tensors, stream):
-    """Tensors just made on the current stream, for a call on `stream`."""
+    """Tensors just made on the current stream, for a call on the stream `stream`."""
     import torch
-    if stream is None:
-        return
     s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
     s.wait_stream(torch.cuda.current_stream())
     for t in tensors:

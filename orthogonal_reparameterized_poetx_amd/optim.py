@@ -148,19 +148,22 @@ class AdamW:
         """(m, v) of the whole set, 256 values a block: the fp32 arrays
         themselves, or what the 8-bit codes stand for (bf16, exact), in `out`
         if that is given: bf16 tensors of as many values (None: not wanted)."""
-        n = self._state["m"].numel()
         if self.state_bits == 32:
             if out is not None:
                 raise ValueError("out goes with an 8-bit state: 32-bit moments are returned as they are held")
             return self._state["m"], self._state["v"]
+        n = self.pset.blocks * BLOCK
         if out is None:
-            out = [torch.empty(n, dtype=torch.bfloat16, device=self.device) for _ in range(2)]
-            L.lend(out, stream)
-        if len(out) != 2:
-            raise ValueError("out is a pair, for m and v")
-        for name, t in zip("mv", out):
-            if t is not None and (_flat(t, "output of " + name, self.device).dtype != torch.bfloat16 or t.numel() != n):
-                raise ValueError("output of %s must be bfloat16 with %d values" % (name, n))
-        m, v = out
+            m, v = [torch.empty(n, dtype=torch.bfloat16, device=self.device) for _ in range(2)]
+            if stream is not None:
+                L.lend((m, v), stream)
+        else:
+            if len(out) != 2:
+                raise ValueError("out is a pair, for m and v")
+            for name, t in zip("mv", out):
+                if t is not None and (_flat(t, "output of " + name, self.device).dtype != torch.bfloat16 or
+                                      t.numel() != n):
+                    raise ValueError("output of %s must be bfloat16 with %d values" % (name, n))
+            m, v = out
         L.poetx_adamw_moments(self.pset, self._cstate, m, v, self._owned.handle(stream))
         return m, v
