@@ -293,6 +293,26 @@ def make_workspace(nbytes, device, stream=None):
         return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
+def pooled_workspace(pool, key, need, device):
+    """The workspace pool[key], replaced where `need` exceeds it.
+
+    Any stream may use it, so one is made and given back only while the
+    device is idle; one that a graph capture has used is not given back, since
+    the graph holds its address."""
+    import torch
+    capturing = torch.cuda.is_current_stream_capturing()
+    ws = pool.get(key)
+    if ws is None or ws.numel() < need:
+        if not capturing:
+            torch.cuda.synchronize(device)
+        elif ws is not None:
+            pool.setdefault("held", []).append(ws)
+        ws = pool[key] = make_workspace(need, device)
+    if capturing and not any(t is ws for t in pool.setdefault("held", [])):
+        pool["held"].append(ws)
+    return ws
+
+
 class Owned:
     """Device buffers of an object whose calls may run on several streams.
 

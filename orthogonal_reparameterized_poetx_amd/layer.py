@@ -56,12 +56,7 @@ class PoetxLayer:
 
     # -- workspaces (grown on demand, reused across calls)
     def workspace(self, op, N=0):
-        need = L.workspace_bytes(self.layer, N, op)
-        ws = self._ws.get(op)
-        if ws is None or ws.numel() < need:
-            ws = L.make_workspace(need, self.device)
-            self._ws[op] = ws
-        return ws
+        return L.pooled_workspace(self._ws, op, L.workspace_bytes(self.layer, N, op), self.device)
 
     def workspace_need(self, op, N=0):
         """Bytes of workspace that op needs for N tokens."""
@@ -270,7 +265,7 @@ def merge_layers_sets(layers, ws=None, stream=None):
                           lay.perm_seed, lay.merges) for lay in layers])
     need = L.merge_sets_workspace_bytes(sets, len(layers))
     if ws is None:
-        ws = L.make_workspace(need, layers[0].device)
+        ws = L.make_workspace(need, layers[0].device, stream)
     elif ws.numel() < need:
         raise ValueError("merge workspace too small")
     L.poetx_merge_blocks_sets(sets, len(layers), ws, stream)
@@ -300,20 +295,14 @@ def build_layer_blocks(layers, kind, stream=None, cnp_terms=0):
         dev = layers[0].device
         if cnp_terms and b <= 256:
             need = L.build_cnp_workspace_bytes(sum(s[1] for s in sets), b)
-            ws = _build_ws.get((dev, b, kind, "cnp"))
-            if ws is None or ws.numel() < need:
-                ws = L.make_workspace(need, dev)
-                _build_ws[(dev, b, kind, "cnp")] = ws
+            ws = L.pooled_workspace(_build_ws, (dev, b, kind, "cnp"), need, dev)
             L.poetx_build_block_sets_cnp(sets, b, cnp_terms, ws, stream)
             continue
         need = L.build_workspace_bytes(sum(s[1] for s in sets), b)
         # one workspace per kind: builds of different kinds may run
         # concurrently on different streams
-        ws = _build_ws.get((dev, b, kind))
-        if need and (ws is None or ws.numel() < need):
-            ws = L.make_workspace(need, dev)
-            _build_ws[(dev, b, kind)] = ws
-        L.poetx_build_block_sets(sets, b, ws if need else None, stream)
+        ws = L.pooled_workspace(_build_ws, (dev, b, kind), need, dev) if need else None
+        L.poetx_build_block_sets(sets, b, ws, stream)
 
 
 _chain_ws = {}
@@ -335,8 +324,5 @@ def chain_rule_layers(layers, grads, accumulate=False, stream=None):
         # one workspace per stream: chain rules of different layers may run
         # concurrently on different streams
         sid = L.stream_handle(stream)
-        ws = _chain_ws.get((dev, b, sid))
-        if need and (ws is None or ws.numel() < need):
-            ws = L.make_workspace(need, dev)
-            _chain_ws[(dev, b, sid)] = ws
-        L.poetx_chain_rule_sets(sets, b, accumulate, ws if need else None, stream)
+        ws = L.pooled_workspace(_chain_ws, (dev, b, sid), need, dev) if need else None
+        L.poetx_chain_rule_sets(sets, b, accumulate, ws, stream)
