@@ -64,6 +64,7 @@ class AdapterSet:
 
     def _make_table(self):
         none = [None] * len(self.A)
+        self._held = [tuple(ts or ()) for ts in (self.A, self.B, self.dA, self.dB)]    # the table has their addresses
         rows = [L.Adapter(L._addr(a), L._addr(b), L._addr(da), L._addr(db), a.shape[0], s)
                 for a, b, da, db, s in zip(self.A, self.B, self.dA or none, self.dB or none, self.scales)]
         dt = L.POETX_BF16 if self.dtype == torch.bfloat16 else L.POETX_F32

@@ -66,6 +66,7 @@ class GradNorm:
 
     def __init__(self, grads, _shared=None):
         self.grads = list(grads)
+        self._held = tuple(self.grads)      # the table has their addresses
         self.table, self.pset, self.device = _shared or _table(None, self.grads, None, None, None)
         self.out = torch.zeros(2, dtype=torch.float32, device=self.device)
         self.ws = L.make_workspace(L.grad_norm_workspace_bytes(self.pset), self.device)
@@ -96,8 +97,10 @@ class AdamW:
                  copies=None, state_bits=32, state=None, step=0):
         if state_bits not in (8, 32):
             raise ValueError("state_bits is 8 or 32")
-        self.params, self.grads, self.copies = list(params), list(grads), copies
-        self.table, self.pset, self.device = _table(self.params, self.grads, copies, lr_mul, weight_decay)
+        self.params, self.grads = list(params), list(grads)
+        self.copies = None if copies is None else list(copies)
+        self._held = tuple(self.params), tuple(self.grads), tuple(self.copies or ())   # the table has their addresses
+        self.table, self.pset, self.device = _table(self.params, self.grads, self.copies, lr_mul, weight_decay)
         self.state_bits, self.steps = state_bits, int(step)
         self.hyper = L.AdamwHyper(float(lr), float(betas[0]), float(betas[1]), float(eps))
         nb = self.pset.blocks

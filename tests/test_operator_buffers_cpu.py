@@ -195,3 +195,23 @@ def test_buffers_of_the_optimizer_know_their_streams(monkeypatch):
     assert a.waits == [current] and {(m.data_ptr(), 7), (v.data_ptr(), 7)} <= set(recorded)
     opt.moments()
     assert a.waits == [current]
+
+
+def test_tensors_of_the_table_live_as_long_as_the_object(monkeypatch):
+    """The table holds their addresses, whatever becomes of the caller's lists."""
+    P = package(monkeypatch)
+    state = dict(m=dev(256), v=dev(256))
+    p, g, c = [dev(200)], [dev(200)], [dev(200, dtype=torch.bfloat16)]
+    refs = [weakref.ref(t) for t in (p[0], g[0], c[0])]
+    opt = P.AdamW(p, g, copies=c, state=state)
+    norm = P.GradNorm(g)
+    for ts in (p, g, c, opt.params, opt.grads, norm.grads):
+        ts.clear()
+    assert all(r() is not None for r in refs)
+    A, B, dA, dB = [dev(4, 64)], [dev(32, 4)], [dev(4, 64)], [dev(32, 4)]
+    refs = [weakref.ref(t[0]) for t in (A, B, dA, dB)]
+    s = P.AdapterSet(32, 64, A, B, [1.0], dA=dA, dB=dB)
+    for ts in (A, B, dA, dB, s.A, s.B, s.dA, s.dB):
+        ts.clear()
+    assert all(r() is not None for r in refs)
+    del opt, norm, s
