@@ -118,8 +118,8 @@ class AdamW:
                                     L._addr(self._state.get("m_exp")), L._addr(self._state.get("v_exp")),
                                     L.POETX_STATE_8BIT if state_bits == 8 else L.POETX_STATE_F32, 0)
         self._owned = L.Owned(self.table, *self._state.values())
-        self._norm = None
-        torch.cuda.current_stream(self.device).synchronize()
+        # here, not at its first call: that may be inside a graph capture (waits for the current stream)
+        self._norm = GradNorm(self.grads, (self.table, self.pset, self.device))
 
     @property
     def lr(self):
@@ -135,8 +135,6 @@ class AdamW:
 
     def grad_norm(self, max_norm=float("inf"), stream=None):
         """(norm, coef) of these gradients, as GradNorm."""
-        if self._norm is None:
-            self._norm = GradNorm(self.grads, (self.table, self.pset, self.device))
         return self._norm(max_norm, stream)
 
     def step(self, coef=None, stream=None):

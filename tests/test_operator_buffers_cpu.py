@@ -215,3 +215,17 @@ def test_tensors_of_the_table_live_as_long_as_the_object(monkeypatch):
         ts.clear()
     assert all(r() is not None for r in refs)
     del opt, norm, s
+
+
+def test_first_gradient_norm_makes_nothing(monkeypatch):
+    """It may be inside a graph capture, which cannot wait for a stream."""
+    P = package(monkeypatch)
+    calls = []
+    monkeypatch.setattr(P._lib, "poetx_grad_norm", lambda *a: calls.append(a))
+    opt = adamw(P, 300, 8)
+    for name in ("zeros", "empty"):
+        monkeypatch.setattr(torch, name, lambda *a, **k: pytest.fail("a buffer is made"))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: pytest.fail("a stream is waited for"))
+    monkeypatch.setattr(P._lib.Owned, "handle", lambda self, stream: 0)
+    norm, coef = opt.grad_norm(1.0)
+    assert len(calls) == 1 and norm.numel() == coef.numel() == 1

@@ -301,3 +301,19 @@ def test_refusals_of_the_classes():
         P.AdamW([a], [a.clone()], betas=(1.0, 0.9)).step()
     with pytest.raises(P.PoetxError):
         P.AdamW([a], [a.clone()], copies=[None], eps=-1.0).step()
+
+
+def test_first_gradient_norm_inside_a_capture():
+    torch = torch_mod()
+    import orthogonal_reparameterized_poetx_amd as P
+    p, g = make(torch, [5000, 333], "f32", "f32", False, 15)
+    opt = P.AdamW(p, g, **HP)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm, coef = opt.grad_norm(1.0)
+    for k in range(3):
+        g[0].add_(k)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = O.grad_norm(host(g), 1.0)
+        assert abs(float(norm) - want[0]) <= 2 * U * want[0] and abs(float(coef) - want[1]) <= 2 * U * want[1]
