@@ -654,6 +654,8 @@ typedef struct {
   void* v_exp; /* POETX_STATE_8BIT only */
   int32_t kind; /* POETX_STATE_F32 or POETX_STATE_8BIT */
   uint32_t reserved; /* must be 0 */
+  uint32_t* skipped; /* [2], zero at first: steps that poetx_adamw_step left out
+                        (see there); NULL: they are counted as taken          */
 } poetx_adamw_state;
 
 typedef struct {
@@ -697,9 +699,15 @@ int poetx_grad_norm(const poetx_param_set* set, float max_norm, float* out, void
  *   m <- b1 m + (1-b1) g;  v <- b2 v + (1-b2) g^2;
  *   p <- p - lr lr_mul (weight_decay p + (m / (1-b1^step)) / (sqrt(v / (1-b2^step)) + eps))
  * in fp32; the update uses the moments before they are rounded to 8 bits.
- *   step  >= 1, the number of this step
+ *   step  >= 1, the number of this step: one more at each call
  *   coef  fp32 [1], device (e.g. out + 1 of poetx_grad_norm), nullable (1).
- *         If it is not finite, nothing is written.
+ *         If it is not finite, no tensor and no moment is written, and with
+ *         state->skipped the steps after it are as if it had not been: step s
+ *         finds the number of such steps before it in skipped[s % 2], takes the
+ *         place of step s less that number in the formula and the dither, and
+ *         leaves the number that step s + 1 finds in skipped[(s + 1) % 2].
+ * step and hyper are values of the launch: a captured graph repeats them, with
+ * one step's bias correction and dither, at every replay.
  */
 int poetx_adamw_step(const poetx_param_set* set, const poetx_adamw_state* state, const poetx_adamw_hyper* hyper,
                      int64_t step, const float* coef, void* stream);

@@ -104,7 +104,8 @@ class ParamSet(ctypes.Structure):
 class AdamwState(ctypes.Structure):
     """poetx_adamw_state: the moments of a set."""
     _fields_ = [("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_exp", ctypes.c_void_p),
-                ("v_exp", ctypes.c_void_p), ("kind", ctypes.c_int32), ("reserved", ctypes.c_uint32)]
+                ("v_exp", ctypes.c_void_p), ("kind", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+                ("skipped", ctypes.c_void_p)]
 
 
 class AdamwHyper(ctypes.Structure):

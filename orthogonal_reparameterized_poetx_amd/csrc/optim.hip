@@ -141,15 +141,30 @@ struct StepArgs {
   const float* coef;
   void *m, *v;
   uint8_t *me, *ve;
+  const uint32_t* before;   // steps skipped before this one, see below; or NULL
+  uint32_t* after;          // and after it
+  int64_t step;
   float lr, b1, b2, ob1, ob2, eps, ibc1, ibc2;
-  uint32_t step;
 };
+
+// 1 / (1 - b^n), n >= 1
+__device__ __forceinline__ float bias_of(float b, uint64_t n) {
+  double p = 1.0, f = b;
+  for (; n; n >>= 1, f *= f)
+    if (n & 1) p *= f;
+  return (float)(1.0 / (1.0 - p));
+}
 
 // A workgroup takes a chunk, each wave one block: small workgroups in the order
 // of the memory.  With four blocks a wave, all loads ahead, 135.6 M values with
 // 8-bit moments took 431 us, with two 418 us, with one 404 us; past the caches and
 // with the hardware's reciprocal and root (one ulp each, on an update that is
 // some 1e-3 of p) 353 us, 6.1 TB/s of the 16 bytes a value.
+// A step whose coefficient is not finite writes nothing, and those after it
+// take its number: step s reads the count of such steps from skipped[s % 2], and its
+// first workgroup leaves the next step's in the other word, which no workgroup
+// of this launch reads.  The host's bias corrections hold for a count of zero;
+// with another they are formed here.
 // The moments are formed with separate roundings (no contraction): the codes
 // of the 8-bit state then follow from the formula alone.
 template <bool Q8>
@@ -157,6 +172,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
 #pragma clang fp contract(off)
   const OptChunk ch = a.chunks[blockIdx.x];
   const float coef = a.coef ? *a.coef : 1.f;
+  const bool finite = fabsf(coef) < INFINITY;
+  const uint32_t skipped = a.before ? *a.before : 0u;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int at = wave * OPT_BLOCK + lane * 4;
   const bool in = wave * OPT_BLOCK < ch.left;   // (a wave without a block reads the chunk's first)
@@ -184,7 +201,14 @@ __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
       v.x[j] = y[j];
     }
   }
-  if (!in || !(fabsf(coef) < INFINITY)) return;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.after) *a.after = skipped + (finite ? 0u : 1u);
+  if (!in || !finite) return;
+  float ibc1 = a.ibc1, ibc2 = a.ibc2;
+  if (__builtin_expect(skipped != 0, 0)) {
+    const uint64_t n = a.step > skipped ? (uint64_t)(a.step - skipped) : 1;   // (1: the counts are not of these steps)
+    ibc1 = bias_of(a.b1, n);
+    ibc2 = bias_of(a.b2, n);
+  }
   if (Q8) {
     em = exp_of(em);
     ev = exp_of(ev);
@@ -194,7 +218,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
       v.x[j] = ev == 255 ? NAN : decode8<false>(vc >> (8 * j) & 255u, ev);
     }
   }
-  const uint32_t h0 = (uint32_t)s * kAlphaPos + a.step * kAlphaStep;
+  const uint32_t h0 = (uint32_t)s * kAlphaPos + ((uint32_t)a.step - skipped) * kAlphaStep;
   uint16_t pb[4], cb[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -204,7 +228,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const StepArgs a) {
     if (j >= left) mj = vj = 0.f;   // padding
     m.x[j] = mj;
     v.x[j] = vj;
-    const float up = (mj * a.ibc1) * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(vj * a.ibc2) + a.eps);
+    const float up = (mj * ibc1) * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(vj * ibc2) + a.eps);
     const float q = p.x[j] - lr * (ch.decay * p.x[j] + up);
     p.x[j] = q;
     // the carry of the dither must not turn infinity or NaN into another value
@@ -419,6 +443,7 @@ int check_state(const poetx_param_set* set, const poetx_adamw_state* st) {
     return host_fail(POETX_EINVAL, "NULL state array");
   if ((reinterpret_cast<uintptr_t>(st->m) & 15) || (reinterpret_cast<uintptr_t>(st->v) & 15))
     return host_fail(POETX_EINVAL, "state arrays must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(st->skipped) & 3) return host_fail(POETX_EINVAL, "state.skipped not aligned to its type");
   return POETX_OK;
 }
 
@@ -517,7 +542,11 @@ int poetx_adamw_step(const poetx_param_set* set, const poetx_adamw_state* state,
   a.ob1 = 1.f - hyper->beta1; a.ob2 = 1.f - hyper->beta2;
   a.ibc1 = (float)(1.0 / (1.0 - std::pow((double)hyper->beta1, (double)step)));
   a.ibc2 = (float)(1.0 / (1.0 - std::pow((double)hyper->beta2, (double)step)));
-  a.step = (uint32_t)step;
+  if (state->skipped) {
+    a.before = state->skipped + (step & 1);
+    a.after = state->skipped + (~step & 1);
+  }
+  a.step = step;
   hipStream_t s = static_cast<hipStream_t>(stream);
   {
     const bool q8 = state->kind == POETX_STATE_8BIT;

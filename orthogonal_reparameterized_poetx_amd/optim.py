@@ -101,7 +101,7 @@ class AdamW:
         self.copies = None if copies is None else list(copies)
         self._held = tuple(self.params), tuple(self.grads), tuple(self.copies or ())   # the table has their addresses
         self.table, self.pset, self.device = _table(self.params, self.grads, self.copies, lr_mul, weight_decay)
-        self.state_bits, self.steps = state_bits, int(step)
+        self.state_bits, self._calls = state_bits, int(step)
         self.hyper = L.AdamwHyper(float(lr), float(betas[0]), float(betas[1]), float(eps))
         nb = self.pset.blocks
         sizes = dict(m=nb * BLOCK, v=nb * BLOCK)
@@ -109,6 +109,7 @@ class AdamW:
             sizes.update(m_exp=nb, v_exp=nb)
         dt = torch.uint8 if state_bits == 8 else torch.float32
         self._state = {}
+        self._skipped = torch.zeros(2, dtype=torch.int32, device=self.device)
         for k, n in sizes.items():
             t = torch.zeros(n, dtype=dt, device=self.device) if state is None else state[k]
             if t.dtype != dt or t.numel() != n:
@@ -116,8 +117,9 @@ class AdamW:
             self._state[k] = _flat(t, "state " + k, self.device)
         self._cstate = L.AdamwState(L._addr(self._state["m"]), L._addr(self._state["v"]),
                                     L._addr(self._state.get("m_exp")), L._addr(self._state.get("v_exp")),
-                                    L.POETX_STATE_8BIT if state_bits == 8 else L.POETX_STATE_F32, 0)
-        self._owned = L.Owned(self.table, *self._state.values())
+                                    L.POETX_STATE_8BIT if state_bits == 8 else L.POETX_STATE_F32, 0,
+                                    self._skipped.data_ptr())
+        self._owned = L.Owned(self.table, self._skipped, *self._state.values())
         # here, not at its first call: that may be inside a graph capture (waits for the current stream)
         self._norm = GradNorm(self.grads, (self.table, self.pset, self.device))
 
@@ -129,6 +131,19 @@ class AdamW:
     def lr(self, value):
         self.hyper.lr = float(value)
 
+    @property
+    def steps(self):
+        """Steps taken: those whose coefficient was not finite are not among them (waits for the device)."""
+        torch.cuda.synchronize(self.device)
+        return self._calls - int(self._skipped[(self._calls + 1) % 2])
+
+    @steps.setter
+    def steps(self, value):
+        torch.cuda.synchronize(self.device)
+        self._calls = int(value)
+        self._skipped.zero_()
+        torch.cuda.synchronize(self.device)
+
     def state(self):
         """The state arrays themselves (save them with self.steps)."""
         return dict(self._state)
@@ -139,11 +154,13 @@ class AdamW:
 
     def step(self, coef=None, stream=None):
         """One step; coef: fp32 tensor of one value on the device that every
-        gradient is multiplied by (nothing is written where it is not finite)."""
+        gradient is multiplied by (where it is not finite, it is as if there
+        had been no step).  The step's number and learning rate are fixed when
+        a graph captures it: every replay repeats them."""
         if coef is not None and (coef.numel() != 1 or coef.dtype != torch.float32 or coef.device != self.device):
             raise ValueError("coef must be one float32 value on %s" % self.device)
-        L.poetx_adamw_step(self.pset, self._cstate, self.hyper, self.steps + 1, coef, self._owned.handle(stream))
-        self.steps += 1
+        L.poetx_adamw_step(self.pset, self._cstate, self.hyper, self._calls + 1, coef, self._owned.handle(stream))
+        self._calls += 1
 
     def moments(self, out=None, stream=None):
         """(m, v) of the whole set, 256 values a block: the fp32 arrays

@@ -108,3 +108,15 @@ def test_reference_rounding_of_8_bits_is_unbiased_and_invertible():
         val = np.where(val == 0, 0.0, val)
         again, _ = O.round8(val, np.arange(256), 7, signed)
         assert np.array_equal(again, val)
+
+
+def test_count_of_skipped_steps_is_checked():
+    P = _P()
+    _, s = P.param_table([_param(P)])
+    s.table = 0x1000
+    hp = P.AdamwHyper(1e-3, 0.9, 0.999, 1e-8)
+    st = P.AdamwState(0x1000, 0x2000, 0x3000, 0x4000, P.POETX_STATE_8BIT, 0, 0x5002)
+    r = ctypes.byref
+    assert P.lib().poetx_adamw_step(r(s), r(st), r(hp), 1, None, None) == -1 and "skipped" in P.last_error()
+    # the states of callers that do not know the field have none
+    assert not P.AdamwState(0x1000, 0x2000, 0x3000, 0x4000, P.POETX_STATE_8BIT, 0).skipped

@@ -317,3 +317,38 @@ def test_first_gradient_norm_inside_a_capture():
         torch.cuda.synchronize()
         want = O.grad_norm(host(g), 1.0)
         assert abs(float(norm) - want[0]) <= 2 * U * want[0] and abs(float(coef) - want[1]) <= 2 * U * want[1]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("first", [0, 100])
+def test_a_skipped_step_is_as_if_it_had_not_been(bits, first):
+    """Steps whose coefficient is not finite write nothing; those after them take the numbers they would have had:
+    bias correction and dither, bit for bit."""
+    torch = torch_mod()
+    import orthogonal_reparameterized_poetx_amd as P
+    sizes = [5000, 7, 1025]
+    p, g = make(torch, sizes, "bf16" if bits == 8 else "f32", "f32", False, 16)
+    q = [t.clone() for t in p]
+    one = P.AdamW(p, g, state_bits=bits, step=first, **HP)
+    two = P.AdamW(q, g, state_bits=bits, step=first, **HP)
+    good, bad = (torch.tensor([x], device="cuda:0") for x in (0.5, float("nan")))
+    for k, skip in enumerate([True, False, True, True, False, False, True, False, True, True]):
+        if skip:
+            one.step(coef=bad if k % 3 else torch.tensor([float("inf")], device="cuda:0"))
+            continue
+        for t in g:
+            t.mul_(-0.75)
+        one.step(coef=good)
+        two.step(coef=good)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(p, q)), k
+        assert all(torch.equal(a, b) for a, b in zip(one.state().values(), two.state().values())), k
+        assert one.steps == two.steps
+    assert one.steps == first + 4
+    # taken up again from what is saved
+    three = P.AdamW(p, g, state_bits=bits, state=one.state(), step=one.steps, **HP)
+    three.step(coef=good)
+    two.step(coef=good)
+    assert all(torch.equal(a, b) for a, b in zip(p, q))
+    one.steps = 7
+    assert one.steps == 7
