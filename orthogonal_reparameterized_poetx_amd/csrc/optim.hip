@@ -13,6 +13,7 @@
 
 #include "../../include/poetx.h"
 #include "global.h"
+#include "grid.h"
 #include "host.h"
 
 namespace poetx {
@@ -534,7 +535,6 @@ int poetx_adamw_step(const poetx_param_set* set, const poetx_adamw_state* state,
   if (!(hyper->eps >= 0.f)) return host_fail(POETX_EINVAL, "eps must not be negative");
   if (set->chunks == 0) return POETX_OK;
   StepArgs a{};
-  a.chunks = chunks_of(set);
   a.coef = coef;
   a.m = state->m; a.v = state->v;
   a.me = static_cast<uint8_t*>(state->m_exp); a.ve = static_cast<uint8_t*>(state->v_exp);
@@ -551,9 +551,12 @@ int poetx_adamw_step(const poetx_param_set* set, const poetx_adamw_state* state,
   {
     const bool q8 = state->kind == POETX_STATE_8BIT;
     HostTimer tm(s, "adamw", 0.0, (q8 ? 16.0 : 28.0) * set->values);
-    const dim3 grid((unsigned)set->chunks), block(256);
-    if (q8) hipLaunchKernelGGL(adamw_kernel<true>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(adamw_kernel<false>, grid, block, 0, s, a);
+    launches(set->chunks, [&](int64_t first, uint32_t number) {
+      a.chunks = chunks_of(set) + first;
+      if (first > 0) a.after = nullptr;   // the first launch has left it
+      if (q8) hipLaunchKernelGGL(adamw_kernel<true>, dim3(number), dim3(256), 0, s, a);
+      else hipLaunchKernelGGL(adamw_kernel<false>, dim3(number), dim3(256), 0, s, a);
+    });
   }
   return host_check_launch("adamw");
 }
@@ -570,10 +573,14 @@ int poetx_adamw_moments(const poetx_param_set* set, const poetx_adamw_state* sta
   hipStream_t s = static_cast<hipStream_t>(stream);
   {
     HostTimer tm(s, "adamw_moments", 0.0, 6.0 * OPT_BLOCK * set->blocks);
-    hipLaunchKernelGGL(moments_kernel, dim3((unsigned)((set->blocks + 15) / 16)), dim3(256), 0, s,
-                       static_cast<const uint8_t*>(state->m), static_cast<const uint8_t*>(state->v),
-                       static_cast<const uint8_t*>(state->m_exp), static_cast<const uint8_t*>(state->v_exp),
-                       static_cast<uint16_t*>(m_out), static_cast<uint16_t*>(v_out), set->blocks);
+    launches((set->blocks + 15) / 16, [&](int64_t first, uint32_t number) {
+      const int64_t at = first * 16, values = at * OPT_BLOCK;
+      hipLaunchKernelGGL(moments_kernel, dim3(number), dim3(256), 0, s, static_cast<const uint8_t*>(state->m) + values,
+                         static_cast<const uint8_t*>(state->v) + values, static_cast<const uint8_t*>(state->m_exp) + at,
+                         static_cast<const uint8_t*>(state->v_exp) + at,
+                         m_out ? static_cast<uint16_t*>(m_out) + values : nullptr,
+                         v_out ? static_cast<uint16_t*>(v_out) + values : nullptr, set->blocks - at);
+    });
   }
   return host_check_launch("adamw moments");
 }
