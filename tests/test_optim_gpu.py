@@ -380,3 +380,36 @@ def test_a_set_of_several_launches():
         assert int(st[k + "_exp"].min()) > 40
     norm, _ = opt.grad_norm()
     assert abs(float(norm) - n ** 0.5) <= 2 * U * n ** 0.5
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-22, 1e-15, 1e-8])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_second_moments_below_the_normal_range(bits, eps):
+    """Gradients whose squares are subnormal in fp32 and an eps that does not cover their root.  The first update is
+    g / (|g| + eps) of the learning rate; v holds a multiple of 2^-149, so its root is off by at most 2^-150 / v of
+    itself beside the roundings (8-bit moments: the update takes them before they are rounded)."""
+    torch = torch_mod()
+    import orthogonal_reparameterized_poetx_amd as P
+    g0 = (2.0 ** np.linspace(-66, -40, 512)).astype(np.float32)
+    g0[1::2] *= -1
+    p = [torch.zeros(512, device="cuda:0")]
+    opt = P.AdamW(p, [torch.from_numpy(g0).to("cuda:0")], betas=(0.5, 0.5), lr=1.0, eps=f32(eps), state_bits=bits)
+    opt.step()
+    got = from_dev(p[0])
+    g = g0.astype(np.float64)
+    assert np.all(np.isfinite(got))
+    want = -g / (np.abs(g) + f32(eps))
+    # v = g^2 / 2, rounded to fp32 twice (the square and its half): 2^-149 at most
+    v_err = 2.0 ** -149 / (g * g / 2) / 2
+    assert np.all(np.abs(got - want) <= np.abs(want) * (24 * U + v_err))
+
+
+def test_no_gradient_yet_and_eps_zero():
+    """0 / 0 is NaN by the formula, in that value alone."""
+    torch = torch_mod()
+    import orthogonal_reparameterized_poetx_amd as P
+    g = torch.tensor([0.0, 0.5, 1.0], device="cuda:0")
+    p = [torch.zeros(3, device="cuda:0")]
+    P.AdamW(p, [g], lr=1.0, eps=0.0).step()
+    got = from_dev(p[0])
+    assert np.isnan(got[0]) and abs(got[2] + 1) <= 24 * U
