@@ -290,27 +290,20 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int rank0 = group * RT * 16;
-  if (rank0 >= ad.rp) return;
-  const int rt_n = (ad.rp - rank0) >> 4;   // rank tiles of this adapter from rank0 on
-  // value of rank tile i and half s that this thread stores
-  auto put = [&](int i, int s, float v) {
+  if (rank0 >= (RT == 1 ? ad.r : ad.rp)) {
+    if (rank0 >= ad.rp) return;
+    // padding alone: zeros, which the expand multiplies, for 16 ranks of 32 tokens: EL ranks
+    // of 16 tokens side by side
     float* T = J.T + ((int64_t)part * a.tiles + w) * a.rpmax * AD_T;
-    const int lanes = a.rpmax < KF ? 16 * (a.rpmax / EL) : 64;
-    const int rank = rank0 + 16 * i + 4 * (tid >> 6) + (tid & 3), c = (tid >> 2) & 15;
-    v = rank < ad.r && 16 * s + c < tile.rows ? v * ad.scale : 0.f;
-    const int kk = rank / KF, gg = rank % KF / EL, e = rank % EL;
-    T[((kk * 2 + s) * lanes + gg * 16 + c) * EL + e] = v;
-  };
-  const RankGroup group_of = rank_group(ad.r, rank0, RT, EL);
-  if (group_of.ranks == 0) {   // padding alone: zeros, which the expand multiplies
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-      if (i < rt_n) {
-        put(i, 0, 0.f);
-        put(i, 1, 0.f);
-      }
+#pragma unroll 1
+    for (int i = tid; i < 16 * AD_T; i += THREADS) {
+      const int rank = rank0 + i / AD_T, t = i % AD_T;
+      T[((rank / KF * 2 + t / 16) * 64 + rank % KF / EL * 16 + t % 16) * EL + rank % EL] = 0.f;
+    }
     return;
   }
+  const int rt_n = (ad.rp - rank0) >> 4;   // rank tiles of this adapter from rank0 on
+  const RankGroup group_of = rank_group(ad.r, rank0, RT, EL);
   const E* X = static_cast<const E*>(J.X) + (int64_t)tile.t0 * J.ldx;
   const E* xend = static_cast<const E*>(J.X) + (int64_t)(a.seg.N - 1) * J.ldx + J.width;
   const E* W = static_cast<const E*>(USEB ? ad.B : ad.A);
@@ -437,6 +430,8 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
     if (!more) break;
   }
   float* red = reinterpret_cast<float*>(lds);
+  float* T = J.T + ((int64_t)part * a.tiles + w) * a.rpmax * AD_T;
+  const int lanes = a.rpmax < KF ? 16 * (a.rpmax / EL) : 64;
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     if (i < rt_n) {
@@ -448,7 +443,10 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs& a, const ShrinkJob
         float v = 0.f;
 #pragma unroll
         for (int q = 0; q < SHRINK_WAVES; ++q) v += red[q * 512 + s * 256 + tid];
-        put(i, s, v);
+        const int rank = rank0 + 16 * i + 4 * (tid >> 6) + (tid & 3), c = (tid >> 2) & 15;
+        v = rank < ad.r && 16 * s + c < tile.rows ? v * ad.scale : 0.f;
+        const int kk = rank / KF, gg = rank % KF / EL, e = rank % EL;
+        T[((kk * 2 + s) * lanes + gg * 16 + c) * EL + e] = v;
       }
       __syncthreads();
     }

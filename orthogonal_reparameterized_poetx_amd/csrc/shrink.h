@@ -30,11 +30,12 @@ constexpr int shrink_lds(int rt, int es) {
 
 // A workgroup's ranks rank0 .. rank0 + 16 rt of an adapter of rank r, and B's rows
 // of them in LDS: pieces of el elements (16 bytes) a row, rows ld elements apart.
-// The ranks are padded to whole matrix steps, so a group may lie wholly in
-// the padding: it has no ranks and no pieces.
+// The ranks are padded to whole matrix steps of 32, so a group of 16 may lie wholly
+// in the padding: it has no ranks and no pieces.  (Larger groups begin at multiples
+// of 32, and the last 32 of the padded ranks hold one of the adapter's.)
 struct RankGroup { int ranks, pieces, ld; };
 POETX_HD inline RankGroup rank_group(int r, int rank0, int rt, int el) {
-  const int left = r - rank0, ranks = left < 0 ? 0 : left < 16 * rt ? left : 16 * rt;
+  const int left = r - rank0, ranks = rt == 1 && left < 0 ? 0 : left < 16 * rt ? left : 16 * rt;
   const int pieces = (ranks + el - 1) / el;
   return RankGroup{ranks, pieces, pieces * el + (el == 4 ? 4 : 0)};
 }
