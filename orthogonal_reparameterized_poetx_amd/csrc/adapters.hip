@@ -177,8 +177,8 @@ struct ShrinkJob {
 };
 struct ListArgs {     // see build_list
   int4* list;
-  int32_t* offs;
-  int cap;
+  int2* offs;
+  int cap, ordered;
 };
 struct TurnArgs {     // see turn_a
   void* At;
@@ -195,7 +195,8 @@ struct ShrinkArgs {
 };                                // grid.x: rank groups of the parts of the jobs; grid.y, z: tiles, then the extra work
 
 // the tiles of each adapter, one adapter after another, for the gradients:
-// entry {t0, rows, adapter, tile index}; offs[a] the first entry of adapter a
+// entry {t0, rows, adapter, tile index}; offs[a]: the first entry of adapter a, and its
+// index; or (ordered) how many adapters before it have tokens
 __device__ __forceinline__ int tiles_of(const AdSegs& g, int s, int& a, int& t0, int& t1) {
   t0 = clamp_token(g.start[s], g.N);
   t1 = clamp_token(g.start[s + 1], g.N);
@@ -203,15 +204,38 @@ __device__ __forceinline__ int tiles_of(const AdSegs& g, int s, int& a, int& t0,
   return a >= 0 && a < g.count && t1 > t0 ? (t1 - t0 + AD_T - 1) / AD_T : 0;
 }
 
+// LDS: a word a wave, and with an order a bit for each adapter
 template <int THREADS>
 __device__ __forceinline__ void build_list(const AdSegs& g, const ListArgs& p, int me, int* cnt) {
   constexpr int WAVES = THREADS / 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int before = 0;
+  unsigned* seen = reinterpret_cast<unsigned*>(cnt + WAVES);   // those before this one that have tokens
+  const int words = p.ordered ? (me + 31) / 32 : 0;
+  int order = me;
+  if (p.ordered) {
+    for (int q = tid; q < words; q += THREADS) seen[q] = 0u;
+    __syncthreads();
+  }
   for (int s = tid; s < g.nseg; s += THREADS) {
     int a, t0, t1;
     const int k = tiles_of(g, s, a, t0, t1);
-    if (k && a < me) before += k;
+    if (k && a < me) {
+      before += k;
+      if (p.ordered) atomicOr(&seen[a >> 5], 1u << (a & 31));
+    }
+  }
+  if (p.ordered) {
+    __syncthreads();
+    int n = 0;
+    for (int q = tid; q < words; q += THREADS) n += __popc(seen[q]);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o);
+    if (lane == 0) cnt[wave] = n;
+    __syncthreads();
+    order = 0;
+    for (int q = 0; q < WAVES; ++q) order += cnt[q];
+    __syncthreads();
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) before += __shfl_xor(before, o);
@@ -221,7 +245,7 @@ __device__ __forceinline__ void build_list(const AdSegs& g, const ListArgs& p, i
   for (int q = 0; q < WAVES; ++q) pos += cnt[q];
   __syncthreads();
   // (segments that overlap, against the contract, could fill more than the list)
-  if (tid == 0) p.offs[me] = pos < p.cap ? pos : p.cap;
+  if (tid == 0) p.offs[me] = make_int2(pos < p.cap ? pos : p.cap, order);
   for (int s0 = 0; s0 < g.nseg; s0 += THREADS) {
     int a = -1, t0 = 0, t1 = 0, k = 0;
     if (s0 + tid < g.nseg) k = tiles_of(g, s0 + tid, a, t0, t1);
@@ -243,7 +267,7 @@ __device__ __forceinline__ void build_list(const AdSegs& g, const ListArgs& p, i
       if (at + i < p.cap) p.list[at + i] = make_int4(t, t1 - t < AD_T ? t1 - t : AD_T, me, t0 / AD_T + s0 + tid + i);
     }
   }
-  if (tid == 0 && me == g.count - 1) p.offs[g.count] = pos < p.cap ? pos : p.cap;
+  if (tid == 0 && me == g.count - 1) p.offs[g.count] = make_int2(pos < p.cap ? pos : p.cap, 0);
 }
 
 __device__ __forceinline__ i16x4 ds_read_tr16a(const uint16_t* p) {
@@ -918,7 +942,7 @@ struct OuterJob {
 struct OuterArgs {
   OuterJob job[2];
   const int4* list;
-  const int32_t* offs;
+  const int2* offs;
   int count, rpmax, run, slabs, slabs0, groups;   // run: list entries of a workgroup; slabs0: slabs of job 0; groups of 16 ranks
   int N;
 };
@@ -932,7 +956,8 @@ struct OuterArgs {
 // gathered into operands of eight tokens by byte permutes; fp32: MFMA step i
 // takes token 4 i + g.  Sums of an adapter within a run go to slot run + adapter
 // (a run begins where the one before it ended, so no two pairs share a
-// slot); a second kernel adds an adapter's slots in order.  A slot is written
+// slot), counted among those with tokens where the set has more than the batch
+// has segments; a second kernel adds an adapter's slots in order.  A slot is written
 // and read as fp32, rank x (n + m): with a run for each wave those bytes
 // outweighed the activations (the same case: 32.8 us).  8192 x (4096 + 11008), rank
 // 16: 54 us, 4.5 TB/s, HBM; 2001 x 4096, rank 64: 15 us.
@@ -953,7 +978,7 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int cb = bx * COLS, col = cb + l16 * EL;
-  const int total = a.offs[a.count];
+  const int total = a.offs[a.count].x;
   int e0 = blockIdx.y * a.run, e1 = e0 + a.run;
   if (e1 > total) e1 = total;
   const E* xend = static_cast<const E*>(J.X) + (int64_t)(a.N - 1) * J.ldx + J.width;
@@ -977,7 +1002,7 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
   };
   while (e0 < e1) {
     const int adapter = a.list[e0].z;
-    const int own = a.offs[adapter + 1], end = own < e1 ? own : e1;
+    const int own = a.offs[adapter + 1].x, end = own < e1 ? own : e1;
     f32x4 acc[EL];
 #pragma unroll
     for (int e = 0; e < EL; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -1037,7 +1062,8 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
         *reinterpret_cast<f32x4*>(&red[wave][l16 * LD + (4 * g + q) * EL + e]) =
             f32x4{acc[e][q], acc[e + 1][q], acc[e + 2][q], acc[e + 3][q]};
     __syncthreads();
-    float* P = J.part + ((int64_t)(blockIdx.y + adapter) * a.rpmax + rank0) * J.width + cb;
+    const int slot = blockIdx.y + a.offs[adapter].y;
+    float* P = J.part + ((int64_t)slot * a.rpmax + rank0) * J.width + cb;
     const int c = tid % COLS;
 #pragma unroll
     for (int r = tid / COLS; r < 16; r += 256 / COLS) {
@@ -1051,7 +1077,7 @@ __global__ __launch_bounds__(256) void adapter_outer_kernel(const OuterArgs a) {
 
 struct ReduceArgs {
   const float* part[2];
-  const int32_t* offs;
+  const int2* offs;
   const AdEntry* table;
   int width[2];          // n (dA), m (dB)
   int rpmax, run, accumulate;
@@ -1067,13 +1093,13 @@ __global__ __launch_bounds__(256) void adapter_reduce_kernel(const ReduceArgs a)
   float* out = job ? e.dB : e.dA;
   const int col = blockIdx.x * 64 + (threadIdx.x & 63);
   if (!out || rank0 >= e.r || (int)blockIdx.x * 64 >= width) return;
-  const int o0 = a.offs[ad], o1 = a.offs[ad + 1];
+  const int o0 = a.offs[ad].x, o1 = a.offs[ad + 1].x;
   const int q0 = o0 / a.run, q1 = o1 > o0 ? (o1 - 1) / a.run : q0 - 1;
   const int64_t stride = (int64_t)a.rpmax * width;
   const int rank = rank0 + (threadIdx.x >> 6) * 4;   // four ranks a thread
   float v[4] = {0.f, 0.f, 0.f, 0.f};
   if (col < width) {
-    const float* p = a.part[job] + (q0 + ad) * stride + (int64_t)rank * width + col;
+    const float* p = a.part[job] + (q0 + a.offs[ad].y) * stride + (int64_t)rank * width + col;
 #pragma unroll 4
     for (int q = q0; q <= q1; ++q, p += stride)
 #pragma unroll
@@ -1169,7 +1195,8 @@ struct AdPlan {
   void* At;
   AdInfo* info;
   int4* list;
-  int32_t* offs;
+  int2* offs;
+  int ordered;         // see ListArgs
   size_t bytes;
 };
 
@@ -1211,7 +1238,8 @@ AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd,
     p.U = reinterpret_cast<float*>(take(tbytes));
     p.At = take((size_t)s->rows * s->n * (f32 ? 4 : 2));
     p.list = reinterpret_cast<int4*>(take((size_t)p.tiles * sizeof(int4)));
-    p.offs = reinterpret_cast<int32_t*>(take((size_t)(s->count + 1) * sizeof(int32_t)));
+    p.offs = reinterpret_cast<int2*>(take((size_t)(s->count + 1) * sizeof(int2)));
+    p.ordered = s->count > nseg;
     // runs of tiles: about 512 workgroups over both gradients
     const int64_t cols = f32 ? 64 : 128;
     p.slabs[0] = (int)((s->n + cols - 1) / cols);
@@ -1219,7 +1247,7 @@ AdPlan plan_adapters(const poetx_adapters* s, int64_t N, int32_t nseg, bool bwd,
     const int64_t run = p.tiles * (p.slabs[0] + p.slabs[1]) * rt_all / 512;
     p.run = (int)(run < 1 ? 1 : run);
     p.runs = (int)((p.tiles + p.run - 1) / p.run);
-    p.slots = p.runs + s->count;
+    p.slots = p.runs + (s->count < nseg ? s->count : nseg);
     p.part[0] = reinterpret_cast<float*>(take((size_t)p.slots * p.rpmax * s->n * sizeof(float)));
     p.part[1] = reinterpret_cast<float*>(take((size_t)p.slots * p.rpmax * s->m * sizeof(float)));
   }
@@ -1370,7 +1398,7 @@ int backward_impl(const poetx_adapters* set, const AdSegs& seg, const void* X, i
   const bool xvec = al16(X) && ldx * es % 16 == 0 && n * es % 16 == 0;
   const bool yvec = al16(dY) && lddy * es % 16 == 0 && m * es % 16 == 0;
   const bool nt = streams(set, seg.N);
-  const ListArgs lists{p.list, p.offs, (int)p.tiles};
+  const ListArgs lists{p.list, p.offs, (int)p.tiles, p.ordered && p.tiles > 0};
   if (p.tiles == 0) {
     hipLaunchKernelGGL(adapter_list_kernel, dim3((unsigned)set->count), dim3(256), 0, s, seg, lists);
   } else {

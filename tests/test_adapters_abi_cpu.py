@@ -77,3 +77,14 @@ def test_call_refusals():
     assert fwd(N=0) == 0 and fwd(nseg=0) == 0
     none = _set(P, ())
     assert fwd(aset=none) == 0 and bwd(aset=none) == 0
+
+
+def test_workspace_goes_by_the_batch_not_by_the_set():
+    """Partial sums of the gradients (rank x (m + n) fp32 each) are for the adapters that have tokens: a large set
+    adds its transposed A (2 bytes, ranks padded to 16) and a few words an adapter."""
+    P = _P()
+    few, many = _set(P, (16,) * 4, m=1024, n=512), _set(P, (16,) * 4000, m=1024, n=512)
+    for N, nseg in ((64, 4), (5000, 4), (64, 64)):
+        extra = P.adapters_workspace_bytes(many, N, nseg, P.OP_BACKWARD) - \
+            P.adapters_workspace_bytes(few, N, nseg, P.OP_BACKWARD)
+        assert extra <= 4000 * (16 * 512 * 2 + 16) + nseg * 16 * (1024 + 512) * 4 + 4096, (N, nseg, extra)

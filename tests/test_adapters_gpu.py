@@ -474,3 +474,19 @@ def test_object_gone_while_its_stream_is_busy():
     held = _fill_freed_memory(torch)                         # on the current stream, at once
     torch.cuda.synchronize()
     assert torch.equal(Y, want) and all(bool(torch.isnan(t).all()) for t in held)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("count,which,lens", [
+    (300, [299, 0, -1, 31, 32, 299, 64, 63], [40, 33, 5, 0, 64, 1, 200, 31]),
+    (40, [39, 17, 5], [700, 0, 650]),
+    (5000, [4999, 2500, 300, 4096], [1, 1, 1, 1]),
+    (3, [2], [500]),
+])
+def test_more_adapters_than_segments(count, which, lens, dtype):
+    """Partial sums lie by an adapter's place among those with tokens; the others' gradients are zero."""
+    start = np.concatenate([[0], np.cumsum(lens)])
+    c = Case(72, 40, [1 + i % 17 for i in range(count)] if count < 1000 else [2] * count, start, which, int(start[-1]),
+             dtype=dtype, seed=count)
+    check_forward(c)
+    check_backward(c)
