@@ -575,6 +575,8 @@ size_t poetx_adapters_workspace_bytes(const poetx_adapters* set, int64_t N, int3
  *   segments without an adapter are left alone.
  * A x is summed in fp32 and kept in fp32 (bf16 sets: as the sum of two bf16
  * values, 16 bits, for the second product); Y is rounded once.  nseg in [0, 1048576].
+ * Values that are not finite stay with their tokens (and adapters, in the
+ * gradients); bf16 sets give NaN also where the formula gives an infinity.
  */
 int poetx_adapters_forward(const poetx_adapters* set, const int32_t* seg_start, const int32_t* seg_adapter,
                            int32_t nseg, const void* X, int64_t ldx, int64_t N, void* Y, int64_t ldy, void* ws,
@@ -682,8 +684,10 @@ int poetx_param_table(const poetx_param* params, int32_t count, void* host_table
  * The 2-norm of all gradients of the set together and the coefficient that
  * clips it, both left on the device:
  *   out[0] = sqrt(sum g^2),  out[1] = min(1, max_norm / (out[0] + 1e-6))
- * summed in fp64 in a fixed order.  If the norm is not finite, out[1] is NaN
- * (poetx_adamw_step then leaves everything as it was).
+ * summed in fp64 in a fixed order.  If the sum is not finite (a gradient is
+ * not), out[1] is NaN, and poetx_adamw_step then leaves everything as it was.
+ * A norm past the range of fp32 gives an infinite out[0]; out[1] is still its
+ * coefficient.
  *   max_norm  > 0 (infinity: no clipping)
  *   out       fp32 [2], device
  *   ws        poetx_grad_norm_workspace_bytes(set) bytes

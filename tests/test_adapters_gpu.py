@@ -490,3 +490,17 @@ def test_more_adapters_than_segments(count, which, lens, dtype):
              dtype=dtype, seed=count)
     check_forward(c)
     check_backward(c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("ranks", [[16, 8], [5, 40]])
+def test_segment_starts_outside_the_batch(ranks, dtype):
+    """Starts below 0 and past N are taken as 0 and N; they do not decrease."""
+    N = 150
+    for start in ([-50, -3, 10, 40, 90, 200], [-2 ** 31, 2 ** 31 - 1], [0, 149, 150, 150, 151, 9999], [-7, 0, 0, 33],
+                  [160, 170, 180], [-9, -5, 0]):
+        which = [(1, 0, -1, 1, 0)[i % 5] for i in range(len(start) - 1)]
+        c = Case(136, 200, ranks, start, which, N, dtype=dtype, seed=len(start))
+        c.start = np.clip(c.start, 0, N)        # (the oracle's; the device has the others)
+        check_forward(c)
+        check_backward(c)

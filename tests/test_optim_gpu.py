@@ -413,3 +413,13 @@ def test_no_gradient_yet_and_eps_zero():
     P.AdamW(p, [g], lr=1.0, eps=0.0).step()
     got = from_dev(p[0])
     assert np.isnan(got[0]) and abs(got[2] + 1) <= 24 * U
+
+
+def test_a_norm_past_the_range_of_fp32():
+    """It reads as infinite; the coefficient is that of the norm itself, here subnormal (steps of 2^-149)."""
+    torch = torch_mod()
+    import orthogonal_reparameterized_poetx_amd as P
+    g = [torch.full((4,), 3e38, device="cuda:0")]
+    n, c = P.GradNorm(g)(2.0)
+    want = 2.0 / (2 * float(np.float32(3e38)))
+    assert np.isinf(float(n)) and abs(float(c) - want) <= 2.0 ** -149
