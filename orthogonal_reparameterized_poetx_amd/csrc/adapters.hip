@@ -285,7 +285,7 @@ __device__ __forceinline__ void turn_a(const AdEntry* table, const TurnArgs& p, 
   const int tid = threadIdx.x, tw = p.tw, c0 = b % p.per * tw, cols = p.n - c0 < tw ? p.n - c0 : tw;
   const int lane = tid & (tw - 1), row = tid / tw, rows = blockDim.x / tw;
   const E* A = static_cast<const E*>(ad.A) + c0;
-  // a row of LDS: one column of A, its ranks; padded to an odd number of dwords
+  // a row of LDS: one column of A, its ranks; padded so that rows of whole matrix steps begin in different banks
   const int ld = ad.r + (sizeof(E) == 2 ? 2 + (ad.r & 1) : 1);
   if (lane < cols)
 #pragma unroll 4
@@ -590,7 +590,7 @@ __device__ __forceinline__ uint4 add_frag(uint4 y, const float* v) {
 // are what in-place updates of Y want: runs of four tiles a workgroup, with W kept
 // in registers and the next tile's Y fetched ahead, took 48.6 us where one
 // tile a workgroup takes 40.4 us, 4.6 TB/s (8192 x 5632, rank 16; 128 columns a wave,
-// whose T is a quarter of the Y it moves; with 64 columns 43.0 us, with 32 46.9 us).
+// a workgroup's T a sixteenth of the Y it moves; with 64 columns 43.0 us, with 32 46.9 us).
 // The update of Y alone, without T and W, takes 38.8 us.
 // The MFMA's rows are the wave's columns, in an order that gives each lane EL
 // neighbouring columns of a token, and the four lanes of a token neighbouring

@@ -3,8 +3,11 @@
 // 32-bit or 8-bit moments.  See include/poetx.h for formats and formulas.
 //
 // Both are streaming passes: per value the step reads p, g, m, v and writes
-// p, m, v, 28 bytes with fp32 everywhere and 16 with 8-bit moments, against
-// about 60 vector instructions, so HBM bounds them.  A table made once on the
+// p, m, v, 28 bytes with fp32 everywhere and 16 with 8-bit moments.  HBM bounds
+// the norm and the step with fp32 moments (15 M values: vector units busy 19 % of
+// the time); with 8-bit moments 105 vector instructions a value, most of them to
+// decode and encode, keep the vector units busy all the time, and they bound it
+// as well (fp32 tensors 6.0 TB/s; bf16 ones, 10 bytes a value, 4.0).  A table made once on the
 // host maps workgroups to tensors: chunk c of the grid is a few state blocks of
 // one tensor, and its record holds all that a workgroup needs of it, so that
 // one scalar load comes before the data.
@@ -104,9 +107,9 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
 
 struct F4 { float x[4]; };
 
-// four values from `at` on; those at or past `left` read as zero.  Reads and
-// writes of a step go past the caches (nontemporal): nothing of it is met again
-// before the next step
+// four values from `at` on; those at or past `left` read as zero.  Values and
+// fp32 moments go past the caches (nontemporal), nothing of them is met again
+// before the next step; 8-bit codes and their exponents go through
 __device__ __forceinline__ F4 load4(const void* base, int64_t at, int left, bool bf, bool vec) {
   F4 r;
   if (vec && left >= 4) {
@@ -160,7 +163,8 @@ __device__ __forceinline__ float bias_of(float b, uint64_t n) {
 // of the memory.  With four blocks a wave, all loads ahead, 135.6 M values with
 // 8-bit moments took 431 us, with two 418 us, with one 404 us; past the caches and
 // with the hardware's reciprocal and root (one ulp each, on an update that is
-// some 1e-3 of p) 353 us, 6.1 TB/s of the 16 bytes a value.
+// some 1e-3 of p) 353 us, 6.1 TB/s of the 16 bytes a value (345 to 370 us on other
+// cards, calls back to back; one at a time under a profiler 380 us).
 // A step whose coefficient is not finite writes nothing, and those after it
 // take its number: step s reads the count of such steps from skipped[s % 2], and its
 // first workgroup leaves the next step's in the other word, which no workgroup

@@ -62,7 +62,8 @@ class GradNorm:
     """norm, coef = GradNorm(grads)(max_norm): the 2-norm of all gradients
     together and min(1, max_norm / (norm + 1e-6)), 0-d fp32 tensors on the
     device that the next call overwrites (coef is NaN where the norm is not
-    finite).  Calls on one object must follow each other on one stream."""
+    finite).  Calls on one object must follow each other on one stream.  The
+    gradients are read in place by address: other tensors need another object."""
 
     def __init__(self, grads, _shared=None):
         self.grads = list(grads)
@@ -84,6 +85,8 @@ class AdamW:
 
     params, grads  lists of contiguous tensors, kept and read in place: a
                    gradient is written into its tensor before every step
+                   (the device table has their addresses: other tensors, such
+                   as gradients allocated anew, need another object)
     lr_mul, weight_decay  one value for each tensor (1 and 0 by default)
     copies         for fp32 tensors: bf16 tensors that receive the updated
                    values (entries may be None)
