@@ -225,21 +225,24 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-_current = None     # torch's functions for the current stream's handle, looked up once
+def _find_current():
+    """A function that gives the current stream's handle, without the Stream object (3 us less) where torch has one."""
+    global _current
+    import torch
+    get, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    torch.cuda.init()
+    _current = (lambda: get(device())) if get and device else lambda: int(torch.cuda.current_stream().cuda_stream)
+    return _current()
+
+
+_current = _find_current    # looked up at the first call
 
 
 def stream_handle(stream):
     """The raw hipStream_t (an int) of a torch.cuda.Stream, a raw handle
     given as an int, or None (torch's current stream)."""
     if stream is None:
-        global _current
-        if _current is None:
-            import torch
-            _current = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda
-        get, cuda = _current
-        if get is not None:     # without the Stream object (3 us less)
-            return get(cuda.current_device())
-        return int(cuda.current_stream().cuda_stream)
+        return _current()
     if type(stream) is int:
         return stream
     if hasattr(stream, "cuda_stream"):
@@ -314,14 +317,20 @@ def pooled_workspace(pool, key, need, device):
     return ws
 
 
+def _torchs_own(stream):
+    """Whether a stream is one of torch's, which live as long as the process."""
+    import torch
+    return stream is None or (hasattr(stream, "cuda_stream") and not isinstance(stream, torch.cuda.ExternalStream))
+
+
 class Owned:
     """Device buffers of an object whose calls may run on several streams.
 
     They live as long as the object, and torch's allocator is told of each
     stream that uses them: once the object is gone it hands none of them out
-    before that stream's queued work is done.  (Not of a stream that is given
-    as a raw handle, which may be gone by then: keep the object until its work
-    is done.)"""
+    before that stream's queued work is done.  (Not of a stream of another
+    owner, a raw handle or an ExternalStream, which may be gone by then: keep
+    the object until its work is done.)"""
 
     def __init__(self, *buffers):
         self._buffers, self._streams = list(buffers), {}
@@ -329,20 +338,17 @@ class Owned:
     def add(self, t):
         self._buffers.append(t)
         for s in self._streams.values():
-            if s is not None:
-                t.record_stream(s)
+            t.record_stream(s)
         return t
 
     def handle(self, stream):
         """Raw handle of a call's stream."""
         h = stream_handle(stream)
-        if h not in self._streams:
+        if h not in self._streams and _torchs_own(stream):
             import torch
-            s = self._streams[h] = torch.cuda.current_stream() if stream is None else \
-                stream if hasattr(stream, "cuda_stream") else None
-            if s is not None:
-                for t in self._buffers:
-                    t.record_stream(s)
+            s = self._streams[h] = torch.cuda.current_stream() if stream is None else stream
+            for t in self._buffers:
+                t.record_stream(s)
         return h
 
 
@@ -351,8 +357,9 @@ def lend(tensors, stream):
     import torch
     s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
     s.wait_stream(torch.cuda.current_stream())
-    for t in tensors:
-        t.record_stream(s)
+    if _torchs_own(stream):
+        for t in tensors:
+            t.record_stream(s)
 
 
 def poetx_build_blocks(theta, nblocks, b, Q32=None, Qbf16=None, QTbf16=None, ws=None, stream=None):

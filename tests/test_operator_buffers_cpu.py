@@ -121,12 +121,16 @@ class Side:
         self.waits.append(other)
 
 
+class External(Side):
+    pass
+
+
 def streams(monkeypatch):
     """The package, the streams that each buffer is recorded on, and the stream that each workspace is made on."""
     P = package(monkeypatch)
     current, recorded, made, context = Side(0), [], {}, [None]
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
-    monkeypatch.setattr(torch.cuda, "ExternalStream", Side)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
     monkeypatch.setattr(P._lib, "stream_handle",
                         lambda s: 0 if s is None else s if isinstance(s, int) else s.cuda_stream)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s.cuda_stream)))
@@ -179,6 +183,11 @@ def test_buffers_of_an_adapter_set_know_their_streams(monkeypatch):
     s.forward(dev(4000, 256, dtype=torch.bfloat16), dev(4000, 512, dtype=torch.bfloat16), *seg, stream=9)
     ws = s.workspace(P.OP_FORWARD, 4000, 1)
     assert made[ws.data_ptr()] == 9 and not [r for r in recorded if r[1] == 9]
+    s.forward(X, Y, *seg, stream=External(9))
+    assert not [r for r in recorded if r[1] == 9]
+    # the same stream, now as one of torch's own: known from here on
+    s.forward(X, Y, *seg, stream=Side(9))
+    assert {(t.data_ptr(), 9) for t in (s.table, ws, wb)} <= set(recorded)
 
 
 def test_buffers_of_the_optimizer_know_their_streams(monkeypatch):
@@ -195,6 +204,9 @@ def test_buffers_of_the_optimizer_know_their_streams(monkeypatch):
     assert a.waits == [current] and {(m.data_ptr(), 7), (v.data_ptr(), 7)} <= set(recorded)
     opt.moments()
     assert a.waits == [current]
+    e = External(9)
+    opt.moments(stream=e)
+    assert e.waits == [current] and not [r for r in recorded if r[1] == 9]
 
 
 def test_tensors_of_the_table_live_as_long_as_the_object(monkeypatch):
